@@ -379,6 +379,125 @@ DSA_API dsa_status_t dsa_mha_prefill(const void* q_idx, const float* w, const vo
                                      int32_t* idx_out, void* out, float* lse,
                                      dsa_stream_t stream);
 
+/* ---- Filling, weighing and trimming the two per-token caches ------------------------
+ * The calls around the path: queries and new tokens get their rotary positions, new
+ * tokens enter both caches in the formats the path reads, every cached token's share
+ * of the attention is accumulated, and caches are trimmed to the tokens that matter.
+ * After a trim a token's slot is no longer its position in the text, so these calls
+ * take rotary positions as an input of their own. */
+
+typedef enum { DSA_BF16 = 0, DSA_FP16 = 1, DSA_FP32 = 2 } dsa_dtype_t;
+
+/* Which dims of the rotated part form pair i: (2i, 2i + 1) or (i, i + rot_dim / 2). */
+typedef enum { DSA_ROPE_HALF = 0, DSA_ROPE_INTERLEAVED = 1, DSA_ROPE_NONE = 2 } dsa_rope_layout_t;
+
+/* Rows of heads of `dim` elements; each head's elements are consecutive. Strides are
+ * in elements, 0 or more (an input stride of 0 reads one row or head for all; output
+ * rows must not overlap). Pointers need the alignment of their element type; 16-byte
+ * aligned pointers, strides, rot_begin and rot_dim (half layout: rot_dim / 2) take
+ * 16-byte accesses. */
+typedef struct {
+  int32_t dtype;          /* dsa_dtype_t of x and out                                   */
+  int32_t layout;         /* DSA_ROPE_HALF or DSA_ROPE_INTERLEAVED                      */
+  int32_t heads, dim;
+  int32_t rot_begin;      /* first rotated dim of a head                                */
+  int32_t rot_dim;        /* rotated dims: even, 2..512, rot_begin + rot_dim <= dim     */
+  float magnitude;        /* factor on the rotated dims (1, or YaRN's attention factor) */
+  int64_t num_rows;
+  int64_t x_row_stride, x_head_stride, out_row_stride, out_head_stride;
+} dsa_rope_desc_t;
+
+/* Rotary positions on a part of every head (the rope part of MLA, report Appendix A):
+ * pair i of row t turns by the angle positions[t] * freqs[i],
+ *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos),
+ * in fp32 from an angle reduced in fp64, rounded once to the output type. The other
+ * dims are copied. Scaled schedules for long contexts are a matter of freqs.
+ *  positions  int32 [num_rows], any sign
+ *  freqs      fp64 [rot_dim / 2]: radians per position
+ *  out        as x: the same rows (in place; the dims outside the rotated part are then
+ *             not touched), or rows that share no element with x's.
+ * dsa_rope_bwd is the backward pass: dx from dout by the transposed rotation (the x
+ * strides are dout's, the out strides dx's). */
+DSA_API dsa_status_t dsa_rope(const void* x, const int32_t* positions, const double* freqs,
+                              const dsa_rope_desc_t* d, void* out, dsa_stream_t stream);
+DSA_API dsa_status_t dsa_rope_bwd(const void* dout, const int32_t* positions, const double* freqs,
+                                  const dsa_rope_desc_t* d, void* dx, dsa_stream_t stream);
+
+/* The new tokens into both caches. Row t of the window (dsa_q_desc_t) is written to the
+ * cache row of its own slot seqlen[b] - q_len[b] + i (seqlens count the new tokens):
+ *  latent cache  dims 0..511 copied, dims 512..575 rotated as dsa_rope does, to bf16
+ *  key cache     dims 0..63 of the key rotated (unless k_layout is DSA_ROPE_NONE), the
+ *                rest as they are, then quantized from fp32: s = max(amax, 2^-120) / 448,
+ *                codes E4M3(k / s) to nearest even; the scale cache gets s. A key with a
+ *                NaN gets NaN codes and a NaN scale.
+ * All other cache rows stay as they were.
+ *  latent_new  bf16 [T] rows of 576, latent_stride elements apart (a multiple of 8)
+ *  k_new       bf16 [T] rows of 128, k_stride elements apart (a multiple of 8)
+ *  positions   int32 [T] rotary positions, or NULL for the slots
+ *  freqs       fp64 [32], magnitude as in dsa_rope
+ *  kv_cache, k_idx, k_scale  the caches, as dsa_sparse_mla_fwd and dsa_indexer_scores
+ *              read them; no two rows of the window may share a slot. */
+DSA_API dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_stride,
+                                      const void* k_new, int64_t k_stride,
+                                      const int32_t* positions, const double* freqs,
+                                      float magnitude, int32_t latent_layout, int32_t k_layout,
+                                      const dsa_kv_desc_t* kv, const dsa_q_desc_t* q,
+                                      void* kv_cache, void* k_idx, float* k_scale,
+                                      dsa_stream_t stream);
+
+/* Attention weight of every cached token, accumulated: for the window's rows t of
+ * sequence b and the entries s of idx[t] inside [0, pos(t)] (as listed; others skipped)
+ *   mass[b][s] += 1/128 sum_h exp(scale q_{t,h} . c_s - lse[t][h]).
+ * A row of the forward adds 1 in all. The result does not depend on the order in which
+ * the GPU runs the rows.
+ *  q, kv_cache, idx, scale as for dsa_sparse_mla_fwd and lse as it wrote it for them
+ *         (a weight above 64 or NaN, which no such lse gives, makes the slot's mass NaN);
+ *         k in [1, 2^20]
+ *  mass   fp32 [batch][mass_ld], mass_ld >= max_ctx, by slot; added to
+ *  workspace  device, 256-byte aligned, dsa_attn_mass_workspace_size() bytes; written
+ *         during the call (stream order), nothing kept in it. With more than 8 rows a
+ *         sequence the rows are summed in units of 2^-40. */
+DSA_API size_t dsa_attn_mass_workspace_size(const dsa_kv_desc_t* kv, const dsa_q_desc_t* q,
+                                            int32_t k);
+DSA_API dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const dsa_kv_desc_t* kv,
+                                   const dsa_q_desc_t* qd, const int32_t* idx, int32_t k,
+                                   float scale, const float* lse, float* mass, int64_t mass_ld,
+                                   void* workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/* Which slots of each sequence stay when its caches are trimmed to `keep` tokens: the
+ * first `sink`, the last `recent`, and of those between them the ones with the most
+ * mass (ties to the lower slot; -0 equals +0; NaN ranks below every number). A sequence
+ * of at most `keep` tokens keeps them all.
+ *  mass      fp32 [batch][mass_ld], mass_ld >= max_ctx, by slot
+ *  kv        batch, max_ctx and seqlens are used
+ *  keep      >= 1 and >= sink + recent
+ *  kept      int32 [batch][keep] out: the slots that stay, ascending, padded with -1
+ *  new_lens  int32 [batch] out: min(seqlen, keep). */
+DSA_API dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_desc_t* kv,
+                                      int32_t keep, int32_t sink, int32_t recent, int32_t* kept,
+                                      int32_t* new_lens, dsa_stream_t stream);
+
+/* The tokens that stay, moved together: slot i < new_lens[b] of the destination takes
+ * slot kept[b][i] of the source in the latent, key and scale caches (all bits as they
+ * are) and in mass; mass of the slots from new_lens[b] to the old length is set to 0,
+ * ready for the tokens that come next. Other cache rows stay as they were.
+ *  kept      int32 [batch][keep], new_lens int32 [batch] as dsa_evict_select writes them;
+ *            new_lens[b] entries are read, each in [0, seqlen), in place also strictly
+ *            ascending. Entries that break this are skipped and reported as
+ *            DSA_ERR_BOUNDS; so is a whole sequence whose lengths are out of range.
+ *  mass      fp32 [batch][mass_ld] or NULL
+ *  dst       NULL: in place (the dst pointers must be NULL, dst_mass_ld is ignored).
+ *            Otherwise the geometry of the destination (batch as kv's, seqlens ignored),
+ *            whose cache arrays may be the source's own as long as no destination slot
+ *            is a slot of any source sequence (pages fresh from the pool).
+ * No two sequences may share the slots they are trimmed in. */
+DSA_API dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, float* mass,
+                                       int64_t mass_ld, const dsa_kv_desc_t* kv,
+                                       const int32_t* kept, int32_t keep, const int32_t* new_lens,
+                                       const dsa_kv_desc_t* dst, void* dst_kv_cache,
+                                       void* dst_k_idx, float* dst_k_scale, float* dst_mass,
+                                       int64_t dst_mass_ld, dsa_stream_t stream);
+
 /* Synchronizes `stream`, then returns and clears the device error word
  * (DSA_OK when no kernel reported a problem since the last call). */
 DSA_API dsa_status_t dsa_get_device_error(dsa_stream_t stream);

@@ -27,3 +27,11 @@ from .dsa_oracle import (  # noqa: F401
     masked_mha,
     absorb_mha_query,
 )
+from .cache_oracle import (  # noqa: F401
+    append_token,
+    attn_weight,
+    cache_at,
+    evict_select,
+    key_codes,
+    rope_rows,
+)

@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdsa.so")
 SOURCES = ["dsa_api.cu"]
 HEADERS = ["ptx.cuh", "rows.cuh", "topk.cuh", "indexer.cuh", "sparse_mla.cuh", "indexer_kl.cuh",
-           "mha_prefill.cuh"]
+           "mha_prefill.cuh", "rope.cuh", "cache.cuh", "evict.cuh", "attn_mass.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

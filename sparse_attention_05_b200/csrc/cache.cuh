@@ -1,0 +1,218 @@
+// cache.cuh -- new tokens into the two per-token caches, and the tokens that stay
+// moved together.
+//
+// Append: the caches hold what the path reads: the latent row [512 latent | 64 rope
+// dims, rotated] in bf16, and the 128-d indexer key in E4M3 with one fp32 scale per
+// token (the two caches of "DeepSeek-V3.2开源技术报告", DSA principle section). The key is
+// quantized from its fp32 rotated value:
+//   s = max(amax |k|, 2^-120) / 448,  code = E4M3(k / s)
+// (round to nearest even), the rule the indexer applies to its queries. Both divisions
+// are IEEE fp32: a reciprocal would move codes at the rounding borders. A token is 1408 B
+// read and 1284 B written, so memory bounds the large calls and one round trip the small
+// ones. One warp a token: lane l owns pair l of the 32 rotated pairs of both rows, so
+// each lane forms one sine and cosine.
+//
+// Compact: slot i of the destination takes slot kept[i] of the source.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "ptx.cuh"
+#include "rope.cuh"
+#include "rows.cuh"
+
+namespace dsa {
+
+constexpr int kAppendWarps = 8;
+
+struct AppendParams {
+  const __nv_bfloat16* latent;  // [T] rows of 576, stride latent_stride
+  const __nv_bfloat16* keys;    // [T] rows of 128, stride key_stride
+  const int32_t* positions;     // [T] or nullptr (the slot)
+  const double* freqs;          // [32]
+  uint8_t* kv;                  // latent cache rows of 1152 B
+  uint8_t* k_idx;               // key rows of 128 B
+  float* k_scale;
+  const int32_t* block_table;
+  const int32_t* seqlens;
+  const int32_t* q_start;
+  int64_t latent_stride, key_stride, window_rows;
+  int32_t max_ctx, q_per_seq, num_q, row_begin, row_count;
+  int32_t paged, page_size, max_pages, num_pages;
+  int32_t latent_interleaved, key_rotated, key_interleaved;
+  float magnitude;
+};
+
+__global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const AppendParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t local = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  if (local >= p.window_rows) return;
+  const int b = (int)(local / p.row_count);
+  const int qi = p.row_begin + (int)(local - (int64_t)b * p.row_count);
+  const SeqRows R = seq_rows(p.q_start, p.seqlens, b, p.q_per_seq, p.num_q, p.max_ctx);
+  if (!R.ok) {
+    if (lane == 0) report_error(kErrBounds);
+    return;
+  }
+  if (qi >= R.q_len) return;
+  const int64_t t = R.t0 + qi;
+  const int slot = R.seqlen - R.q_len + qi;
+  int64_t row = (int64_t)b * p.max_ctx + slot;
+  if (p.paged) {
+    const int pg = __ldg(p.block_table + (int64_t)b * p.max_pages + slot / p.page_size);
+    if (pg < 0 || pg >= p.num_pages) {
+      if (lane == 0) report_error(kErrBounds);
+      return;
+    }
+    row = (int64_t)pg * p.page_size + slot % p.page_size;
+  }
+  const __nv_bfloat16* lat = p.latent + t * p.latent_stride;
+  const __nv_bfloat16* key = p.keys + t * p.key_stride;
+  uint4* dst = reinterpret_cast<uint4*>(p.kv + row * 1152);
+  const uint4 n0 = __ldg(reinterpret_cast<const uint4*>(lat) + lane);
+  const uint4 n1 = __ldg(reinterpret_cast<const uint4*>(lat) + 32 + lane);
+  // the lane's pair of each rotated part, and its two plain key dims
+  const int l0 = p.latent_interleaved ? 2 * lane : lane, l1 = p.latent_interleaved ? l0 + 1 : lane + 32;
+  const int k0 = p.key_interleaved ? 2 * lane : lane, k1 = p.key_interleaved ? k0 + 1 : lane + 32;
+  float la = __bfloat162float(lat[512 + l0]), lb = __bfloat162float(lat[512 + l1]);
+  float ka = __bfloat162float(key[k0]), kb = __bfloat162float(key[k1]);
+  const float2 kc = __bfloat1622float2(
+      *reinterpret_cast<const __nv_bfloat162*>(key + 64 + 2 * lane));
+  const float2 cs = rope_turn(p.positions ? __ldg(p.positions + t) : slot, __ldg(p.freqs + lane),
+                              p.magnitude);
+  dst[lane] = n0;
+  dst[32 + lane] = n1;
+  __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(dst) + 512;
+  rope[l0] = __float2bfloat16_rn(la * cs.x - lb * cs.y);
+  rope[l1] = __float2bfloat16_rn(la * cs.y + lb * cs.x);
+  if (p.key_rotated) {
+    const float a = ka * cs.x - kb * cs.y;
+    kb = ka * cs.y + kb * cs.x;
+    ka = a;
+  }
+  // the largest magnitude by its bits: a NaN anywhere makes the scale a NaN
+  auto bits = [](float v) { return __float_as_uint(v) & 0x7fffffffu; };
+  const uint32_t m = __reduce_max_sync(0xffffffffu, max(max(bits(ka), bits(kb)),
+                                                        max(bits(kc.x), bits(kc.y))));
+  const float amax = __uint_as_float(m);
+  const float scale = __fdiv_rn(amax < 0x1p-120f ? 0x1p-120f : amax, 448.0f);
+  const uint16_t rot = cvt_e4m3x2(__fdiv_rn(ka, scale), __fdiv_rn(kb, scale));
+  uint8_t* codes = p.k_idx + row * 128;
+  codes[k0] = (uint8_t)rot;
+  codes[k1] = (uint8_t)(rot >> 8);
+  *reinterpret_cast<uint16_t*>(codes + 64 + 2 * lane) =
+      cvt_e4m3x2(__fdiv_rn(kc.x, scale), __fdiv_rn(kc.y, scale));
+  if (lane == 0) p.k_scale[row] = scale;
+}
+
+// ---- compact ---------------------------------------------------------------------------
+// Moving in place: kept is ascending, so kept[i] >= i, and a chunk's destinations lie
+// below every later chunk's sources. One CTA takes a column slice of a sequence through
+// its chunks in order: it loads a chunk, waits for all its threads, and stores it. The
+// slices are independent of each other, which is where the parallelism comes from: nine
+// of 128 B of the latent row, one of the key row, one of scale and mass.
+constexpr int kCompactThreads = 256;
+constexpr int kCompactSlices = 11;
+constexpr int kCompactUnroll = 4;
+
+struct CompactParams {
+  const uint8_t* kv;
+  const uint8_t* k_idx;
+  const float* k_scale;
+  const float* mass;           // or nullptr
+  uint8_t* to_kv;
+  uint8_t* to_k_idx;
+  float* to_k_scale;
+  float* to_mass;
+  const int32_t* kept;         // [batch][keep]
+  const int32_t* new_lens;     // [batch]
+  const int32_t* seqlens;      // [batch] or nullptr
+  const int32_t* table;        // paged source
+  const int32_t* to_table;     // paged destination
+  int64_t mass_ld, to_mass_ld;
+  int32_t keep, in_place;
+  int32_t max_ctx, page_size, max_pages, num_pages;
+  int32_t to_max_ctx, to_page_size, to_max_pages, to_num_pages;
+};
+
+// Row of the cache arrays that holds a slot, -1 for a page outside the cache.
+__device__ __forceinline__ int64_t cache_row(const int32_t* table, int b, int slot, int max_ctx,
+                                             int page_size, int max_pages, int num_pages) {
+  if (!table) return (int64_t)b * max_ctx + slot;
+  const int pg = __ldg(table + (int64_t)b * max_pages + slot / page_size);
+  if (pg < 0 || pg >= num_pages) return -1;
+  return (int64_t)pg * page_size + slot % page_size;
+}
+
+__global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const CompactParams p) {
+  const int b = blockIdx.x, slice = blockIdx.y, tid = threadIdx.x;
+  const int len = p.seqlens ? __ldg(p.seqlens + b) : p.max_ctx;
+  const int n = __ldg(p.new_lens + b);
+  if (len < 0 || len > p.max_ctx || n < 0 || n > p.keep || n > len || n > p.to_max_ctx) {
+    if (tid == 0) report_error(kErrBounds);
+    return;
+  }
+  const int32_t* kept = p.kept + (int64_t)b * p.keep;
+  // the source and destination row of entry i, both -1 where the entry is out of range
+  auto rows_of = [&](int i, int64_t& src, int64_t& dst, int& slot) {
+    src = dst = -1;
+    if (i >= n) return;
+    slot = __ldg(kept + i);
+    bool ok = slot >= 0 && slot < len;
+    if (p.in_place) ok = ok && slot >= i && (i == 0 || slot > __ldg(kept + i - 1));
+    if (ok) {
+      src = cache_row(p.table, b, slot, p.max_ctx, p.page_size, p.max_pages, p.num_pages);
+      dst = cache_row(p.to_table, b, i, p.to_max_ctx, p.to_page_size, p.to_max_pages,
+                      p.to_num_pages);
+    }
+    if (src < 0 || dst < 0) {
+      report_error(kErrBounds);
+      src = dst = -1;
+    }
+  };
+  if (slice < 10) {  // 128 B a row, eight threads a row
+    const int piece = tid & 7;
+    const int64_t pitch = slice < 9 ? 1152 : 128;
+    const uint8_t* from = (slice < 9 ? p.kv + slice * 128 : p.k_idx) + piece * 16;
+    uint8_t* to = (slice < 9 ? p.to_kv + slice * 128 : p.to_k_idx) + piece * 16;
+    constexpr int kRows = kCompactThreads / 8;
+    for (int i0 = 0; i0 < n; i0 += kRows * kCompactUnroll) {
+      uint4 v[kCompactUnroll];
+      int64_t dst[kCompactUnroll];
+#pragma unroll
+      for (int u = 0; u < kCompactUnroll; ++u) {
+        int64_t src;
+        int slot;
+        rows_of(i0 + u * kRows + (tid >> 3), src, dst[u], slot);
+        if (src >= 0) v[u] = *reinterpret_cast<const uint4*>(from + src * pitch);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kCompactUnroll; ++u)
+        if (dst[u] >= 0) *reinterpret_cast<uint4*>(to + dst[u] * pitch) = v[u];
+    }
+    return;
+  }
+  for (int i0 = 0; i0 < n; i0 += kCompactThreads) {
+    int64_t src, dst;
+    int slot = 0;
+    float s = 0.f, m = 0.f;
+    rows_of(i0 + tid, src, dst, slot);
+    if (src >= 0) {
+      s = p.k_scale[src];
+      if (p.mass) m = p.mass[(int64_t)b * p.mass_ld + slot];
+    }
+    __syncthreads();
+    if (dst >= 0) {
+      p.to_k_scale[dst] = s;
+      if (p.mass) p.to_mass[(int64_t)b * p.to_mass_ld + i0 + tid] = m;
+    }
+  }
+  if (p.mass) {
+    __syncthreads();
+    for (int i = n + tid; i < min(len, p.to_max_ctx); i += kCompactThreads)
+      p.to_mass[(int64_t)b * p.to_mass_ld + i] = 0.f;
+  }
+}
+
+}  // namespace dsa

@@ -19,6 +19,10 @@
 #include "sparse_mla.cuh"
 #include "indexer_kl.cuh"
 #include "mha_prefill.cuh"
+#include "rope.cuh"
+#include "cache.cuh"
+#include "evict.cuh"
+#include "attn_mass.cuh"
 
 using namespace dsa;
 
@@ -798,6 +802,183 @@ __global__ void wait_timeout_selftest_kernel(uint64_t timeout_ns) {
   mbar_wait(smem_u32(&bar), 0, timeout_ns, &abort_flag);
 }
 
+
+// ---- rotary positions --------------------------------------------------------------
+int rope_elem_bytes(int32_t dtype) {
+  return dtype == DSA_BF16 || dtype == DSA_FP16 ? 2 : dtype == DSA_FP32 ? 4 : 0;
+}
+
+// Rows of `out` must not overlap each other, nor x unless they are the same rows.
+// Strides count only where there is more than one row or head.
+struct RopeSpan {
+  int64_t inner, inner_n, outer, outer_n, extent;  // extent: elements from first to last
+};
+
+RopeSpan rope_span(int64_t row, int64_t rows, int64_t head, int64_t heads, int64_t dim) {
+  RopeSpan s{};
+  if (rows <= 1) row = 0;
+  if (heads <= 1) head = 0;
+  s.extent = (rows - 1) * row + (heads - 1) * head + dim;
+  if (heads <= 1 || (rows > 1 && row < head)) {
+    s.inner = row, s.inner_n = rows, s.outer = head, s.outer_n = heads;
+  } else {
+    s.inner = head, s.inner_n = heads, s.outer = row, s.outer_n = rows;
+  }
+  return s;
+}
+
+dsa_status_t launch_rope(const void* x, const int32_t* positions, const double* freqs,
+                         const dsa_rope_desc_t* d, void* out, bool transposed,
+                         cudaStream_t stream) {
+  if (!d) return DSA_ERR_INVALID_ARG;
+  const int es = rope_elem_bytes(d->dtype);
+  if (!es || (d->layout != DSA_ROPE_HALF && d->layout != DSA_ROPE_INTERLEAVED))
+    return DSA_ERR_INVALID_ARG;
+  if (d->num_rows < 0 || d->heads < 1 || d->dim < 1 || d->rot_begin < 0 || d->rot_dim < 2 ||
+      d->rot_dim % 2 || d->rot_begin > d->dim - d->rot_dim)
+    return DSA_ERR_INVALID_ARG;
+  if (d->rot_dim > kRopeMaxRot || d->num_rows >= (1ll << 31) || d->dim > (1 << 20) ||
+      d->heads > (1 << 20))
+    return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!(std::fabs(d->magnitude) < 1e30f)) return DSA_ERR_INVALID_ARG;
+  if (d->num_rows == 0) return DSA_OK;
+  if (!x || !positions || !freqs || !out) return DSA_ERR_INVALID_ARG;
+  const int64_t strides[4] = {d->x_row_stride, d->x_head_stride, d->out_row_stride,
+                              d->out_head_stride};
+  for (int64_t s : strides)
+    if (s < 0 || s > (1ll << 40)) return DSA_ERR_INVALID_ARG;
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
+  if (xa % es || oa % es || (reinterpret_cast<uintptr_t>(positions) & 3) ||
+      (reinterpret_cast<uintptr_t>(freqs) & 7))
+    return DSA_ERR_INVALID_ARG;
+  const RopeSpan xs = rope_span(strides[0], d->num_rows, strides[1], d->heads, d->dim);
+  const RopeSpan os = rope_span(strides[2], d->num_rows, strides[3], d->heads, d->dim);
+  if (os.inner_n > 1 && os.inner < d->dim) return DSA_ERR_INVALID_ARG;
+  if (os.outer_n > 1 && os.outer < (os.inner_n - 1) * os.inner + d->dim)
+    return DSA_ERR_INVALID_ARG;
+  const bool same = (d->num_rows == 1 || strides[0] == strides[2]) &&
+                    (d->heads == 1 || strides[1] == strides[3]);
+  const bool in_place = xa == oa && same;
+  if (!in_place && xa < oa + os.extent * es && oa < xa + xs.extent * es) {
+    // interleaved views of one buffer: every row of one between two rows of the other
+    if (!same || os.inner_n < 2 || (oa > xa ? oa - xa : xa - oa) % es) return DSA_ERR_INVALID_ARG;
+    const int64_t step = (int64_t)((oa > xa ? oa - xa : xa - oa) / es) % os.inner;
+    if (step < d->dim || step > os.inner - d->dim) return DSA_ERR_INVALID_ARG;
+    if (os.outer_n > 1 && os.outer % os.inner) return DSA_ERR_INVALID_ARG;
+  }
+  RopeParams p{};
+  p.x = x;
+  p.out = out;
+  p.positions = positions;
+  p.freqs = freqs;
+  p.x_row = strides[0], p.x_head = strides[1], p.o_row = strides[2], p.o_head = strides[3];
+  p.rows = d->num_rows;
+  p.heads = d->heads;
+  p.half = d->rot_dim / 2;
+  p.rot_begin = d->rot_begin;
+  p.dim = d->dim;
+  p.copy = !in_place && d->dim > d->rot_dim;
+  p.magnitude = d->magnitude;
+  p.sign = transposed ? -1.f : 1.f;
+  const bool inter = d->layout == DSA_ROPE_INTERLEAVED;
+  // 16-byte accesses where every row and run starts on a 16-byte boundary
+  const int v = 16 / es;
+  bool wide = !((xa | oa) & 15) && d->rot_begin % v == 0 &&
+              (inter ? d->rot_dim : p.half) % v == 0 && (!p.copy || d->dim % v == 0);
+  for (int i = 0; i < 4; ++i)
+    wide = wide && ((i & 1 ? d->heads : d->num_rows) == 1 || strides[i] % v == 0);
+  const int vec = wide ? v : 1;
+  const int pairs = inter ? std::max(1, vec / 2) : vec;
+  const int64_t units = p.half / pairs + (p.copy ? (d->dim - d->rot_dim) / vec : 0);
+  const int64_t total = units * d->heads * d->num_rows;
+  const int64_t target = total >= 1184 * 1024 ? 1024 : kRopeThreads;
+  const int64_t per_row = units * d->heads;
+  p.rows_per_block = (int)std::max<int64_t>(
+      1, std::min({target / per_row, (int64_t)kRopeMaxRows, (int64_t)(kRopeTable / p.half)}));
+  p.heads_per_block = (int)std::max<int64_t>(1, std::min<int64_t>(d->heads, target / units));
+  const int64_t gx = (d->num_rows + p.rows_per_block - 1) / p.rows_per_block;
+  int64_t gy = (d->heads + p.heads_per_block - 1) / p.heads_per_block;
+  if (gy > 65535) {
+    p.heads_per_block = (d->heads + 65534) / 65535;
+    gy = (d->heads + p.heads_per_block - 1) / p.heads_per_block;
+  }
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  auto go = [&](auto kernel) { kernel<<<grid, kRopeThreads, 0, stream>>>(p); };
+  if (d->dtype == DSA_FP32) {
+    if (inter) wide ? go(rope_kernel<float, 4, true>) : go(rope_kernel<float, 1, true>);
+    else wide ? go(rope_kernel<float, 4, false>) : go(rope_kernel<float, 1, false>);
+  } else if (d->dtype == DSA_BF16) {
+    if (inter) wide ? go(rope_kernel<__nv_bfloat16, 8, true>) : go(rope_kernel<__nv_bfloat16, 1, true>);
+    else wide ? go(rope_kernel<__nv_bfloat16, 8, false>) : go(rope_kernel<__nv_bfloat16, 1, false>);
+  } else {
+    if (inter) wide ? go(rope_kernel<__half, 8, true>) : go(rope_kernel<__half, 1, true>);
+    else wide ? go(rope_kernel<__half, 8, false>) : go(rope_kernel<__half, 1, false>);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+// ---- attention mass ----------------------------------------------------------------
+// Rows of a sequence up to which its rows' weights are added one row after another.
+constexpr int kMassFewRows = 8;
+
+size_t mass_workspace(const Geometry& g, int k) {
+  return g.row_count <= kMassFewRows ? align256((size_t)g.batch * g.row_count * k * 4)
+                                     : align256((size_t)g.batch * g.max_ctx * 8);
+}
+
+dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometry& g,
+                              const int32_t* idx, int k, float scale, const float* lse,
+                              float* mass, int64_t mass_ld, void* workspace,
+                              cudaStream_t stream) {
+  static DeviceOnce once;
+  const cudaError_t attr_err = once_per_device(once, [] {
+    return cudaFuncSetAttribute(attn_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kMassSmemBytes);
+  });
+  if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
+  MassParams p{};
+  p.kv = reinterpret_cast<const uint8_t*>(kv_cache);
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.idx = idx;
+  p.lse = lse;
+  p.block_table = g.block_table;
+  p.seqlens = g.seqlens;
+  p.q_start = g.q_start;
+  const bool few = g.row_count <= kMassFewRows;
+  if (few)
+    p.p_out = reinterpret_cast<float*>(workspace);
+  else
+    p.sums = reinterpret_cast<unsigned long long*>(workspace);
+  p.mass = mass;
+  p.mass_ld = mass_ld;
+  p.k = k;
+  p.batch = g.batch;
+  p.max_ctx = g.max_ctx;
+  p.q_per_seq = g.q_per_seq;
+  p.num_q = g.num_q;
+  p.row_begin = g.row_begin;
+  p.row_count = g.row_count;
+  p.paged = g.layout == DSA_KV_PAGED;
+  p.page_size = g.page_size;
+  p.max_pages = g.max_pages;
+  p.num_pages = g.num_pages;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.timeout_ns = g_timeout_ns.load();
+  if (!few) {
+    const cudaError_t e = cudaMemsetAsync(workspace, 0, (size_t)g.batch * g.max_ctx * 8, stream);
+    if (e != cudaSuccess) return DSA_ERR_CUDA;
+  }
+  attn_mass_kernel<<<(unsigned)((int64_t)g.batch * g.row_count), kMassThreads, kMassSmemBytes,
+                     stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+  if (few)
+    mass_add_rows_kernel<<<(unsigned)g.batch, 512, 0, stream>>>(p);
+  else
+    mass_add_sums_kernel<<<dim3((unsigned)((g.max_ctx + 255) / 256), (unsigned)g.batch), 256, 0,
+                           stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
 }  // namespace
 
 extern "C" {
@@ -1242,5 +1423,165 @@ dsa_status_t dsa_topk(const float* scores, int64_t ld, const dsa_kv_desc_t* kv,
   return launch_topk(scores, ld, g, g.row_begin, g.row_count, k, idx, (cudaStream_t)stream);
 }
 
-}  // extern "C"
+dsa_status_t dsa_rope(const void* x, const int32_t* positions, const double* freqs,
+                      const dsa_rope_desc_t* d, void* out, dsa_stream_t stream) {
+  return launch_rope(x, positions, freqs, d, out, false, (cudaStream_t)stream);
+}
 
+dsa_status_t dsa_rope_bwd(const void* dout, const int32_t* positions, const double* freqs,
+                          const dsa_rope_desc_t* d, void* dx, dsa_stream_t stream) {
+  return launch_rope(dout, positions, freqs, d, dx, true, (cudaStream_t)stream);
+}
+
+dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_stride, const void* k_new,
+                              int64_t k_stride, const int32_t* positions, const double* freqs,
+                              float magnitude, int32_t latent_layout, int32_t k_layout,
+                              const dsa_kv_desc_t* kv, const dsa_q_desc_t* q, void* kv_cache,
+                              void* k_idx, float* k_scale, dsa_stream_t stream) {
+  Geometry g;
+  dsa_status_t st = check_geometry(kv, q, &g);
+  if (st != DSA_OK) return st;
+  if (!kv_cache || !k_idx || !k_scale || !freqs) return DSA_ERR_INVALID_ARG;
+  if ((latent_layout != DSA_ROPE_HALF && latent_layout != DSA_ROPE_INTERLEAVED) ||
+      (k_layout != DSA_ROPE_NONE && k_layout != DSA_ROPE_HALF && k_layout != DSA_ROPE_INTERLEAVED))
+    return DSA_ERR_INVALID_ARG;
+  if (!(std::fabs(magnitude) < 1e30f)) return DSA_ERR_INVALID_ARG;
+  if (g.num_q == 0) return DSA_OK;
+  if (!latent_new || !k_new) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(latent_new) || !aligned16(k_new) || !aligned16(kv_cache) || !aligned16(k_idx) ||
+      (reinterpret_cast<uintptr_t>(k_scale) & 3) || (reinterpret_cast<uintptr_t>(freqs) & 7) ||
+      (reinterpret_cast<uintptr_t>(positions) & 3))
+    return DSA_ERR_INVALID_ARG;
+  if (latent_stride < 576 || latent_stride % 8 || k_stride < 128 || k_stride % 8)
+    return DSA_ERR_INVALID_ARG;
+  AppendParams p{};
+  p.latent = reinterpret_cast<const __nv_bfloat16*>(latent_new);
+  p.keys = reinterpret_cast<const __nv_bfloat16*>(k_new);
+  p.positions = positions;
+  p.freqs = freqs;
+  p.kv = reinterpret_cast<uint8_t*>(kv_cache);
+  p.k_idx = reinterpret_cast<uint8_t*>(k_idx);
+  p.k_scale = k_scale;
+  p.block_table = g.block_table;
+  p.seqlens = g.seqlens;
+  p.q_start = g.q_start;
+  p.latent_stride = latent_stride;
+  p.key_stride = k_stride;
+  p.window_rows = (int64_t)g.batch * g.row_count;
+  p.max_ctx = g.max_ctx;
+  p.q_per_seq = g.q_per_seq;
+  p.num_q = g.num_q;
+  p.row_begin = g.row_begin;
+  p.row_count = g.row_count;
+  p.paged = g.layout == DSA_KV_PAGED;
+  p.page_size = g.page_size;
+  p.max_pages = g.max_pages;
+  p.num_pages = g.num_pages;
+  p.latent_interleaved = latent_layout == DSA_ROPE_INTERLEAVED;
+  p.key_rotated = k_layout != DSA_ROPE_NONE;
+  p.key_interleaved = k_layout == DSA_ROPE_INTERLEAVED;
+  p.magnitude = magnitude;
+  const int64_t blocks = (p.window_rows + kAppendWarps - 1) / kAppendWarps;
+  cache_append_kernel<<<(unsigned)blocks, kAppendWarps * 32, 0, (cudaStream_t)stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+size_t dsa_attn_mass_workspace_size(const dsa_kv_desc_t* kv, const dsa_q_desc_t* q, int32_t k) {
+  Geometry g;
+  if (check_geometry(kv, q, &g) != DSA_OK || k < 1 || k > (1 << 20)) return 0;
+  return mass_workspace(g, k);
+}
+
+dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const dsa_kv_desc_t* kv,
+                           const dsa_q_desc_t* qd, const int32_t* idx, int32_t k, float scale,
+                           const float* lse, float* mass, int64_t mass_ld, void* workspace,
+                           size_t workspace_bytes, dsa_stream_t stream) {
+  Geometry g;
+  dsa_status_t st = check_geometry(kv, qd, &g);
+  if (st != DSA_OK) return st;
+  if (k < 1 || k > (1 << 20)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!(scale > 0.f) || !(scale < 1e30f) || mass_ld < g.max_ctx) return DSA_ERR_INVALID_ARG;
+  if (!mass || !kv_cache) return DSA_ERR_INVALID_ARG;
+  if (g.num_q == 0) return DSA_OK;
+  if (!q || !idx || !lse) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv_cache) || (reinterpret_cast<uintptr_t>(mass) & 3))
+    return DSA_ERR_INVALID_ARG;
+  if (g.batch > 65535) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < mass_workspace(g, k))
+    return DSA_ERR_WORKSPACE;
+  return launch_attn_mass(q, kv_cache, g, idx, k, scale, lse, mass, mass_ld, workspace,
+                          (cudaStream_t)stream);
+}
+
+dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_desc_t* kv,
+                              int32_t keep, int32_t sink, int32_t recent, int32_t* kept,
+                              int32_t* new_lens, dsa_stream_t stream) {
+  dsa_q_desc_t qd{kv ? kv->batch : 0, 1, 0, 0, nullptr};  // keys only: one nominal row each
+  Geometry g;
+  dsa_status_t st = check_geometry(kv, &qd, &g);
+  if (st != DSA_OK) return st;
+  if (!mass || !kept || !new_lens || mass_ld < g.max_ctx) return DSA_ERR_INVALID_ARG;
+  if (keep < 1 || sink < 0 || recent < 0 || sink > keep || recent > keep - sink)
+    return DSA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(mass) & 3) || (reinterpret_cast<uintptr_t>(kept) & 3) ||
+      (reinterpret_cast<uintptr_t>(new_lens) & 3))
+    return DSA_ERR_INVALID_ARG;
+  EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent};
+  evict_select_kernel<<<(unsigned)g.batch, kEvictThreads, 0, (cudaStream_t)stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, float* mass,
+                               int64_t mass_ld, const dsa_kv_desc_t* kv, const int32_t* kept,
+                               int32_t keep, const int32_t* new_lens, const dsa_kv_desc_t* dst,
+                               void* dst_kv_cache, void* dst_k_idx, float* dst_k_scale,
+                               float* dst_mass, int64_t dst_mass_ld, dsa_stream_t stream) {
+  dsa_q_desc_t qd{kv ? kv->batch : 0, 1, 0, 0, nullptr};
+  Geometry g, t;
+  dsa_status_t st = check_geometry(kv, &qd, &g);
+  if (st != DSA_OK) return st;
+  if (!kv_cache || !k_idx || !k_scale || !kept || !new_lens || keep < 1) return DSA_ERR_INVALID_ARG;
+  if (!dst) {  // in place
+    if (dst_kv_cache || dst_k_idx || dst_k_scale || dst_mass) return DSA_ERR_INVALID_ARG;
+    t = g;
+    dst_kv_cache = kv_cache, dst_k_idx = k_idx, dst_k_scale = k_scale;
+    dst_mass = mass, dst_mass_ld = mass_ld;
+  } else {
+    st = check_geometry(dst, &qd, &t);
+    if (st != DSA_OK) return st;
+    if (!dst_kv_cache || !dst_k_idx || !dst_k_scale || !mass != !dst_mass)
+      return DSA_ERR_INVALID_ARG;
+  }
+  if (mass && (mass_ld < g.max_ctx || dst_mass_ld < t.max_ctx)) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(kv_cache) || !aligned16(k_idx) || !aligned16(dst_kv_cache) ||
+      !aligned16(dst_k_idx))
+    return DSA_ERR_INVALID_ARG;
+  CompactParams p{};
+  p.kv = reinterpret_cast<const uint8_t*>(kv_cache);
+  p.k_idx = reinterpret_cast<const uint8_t*>(k_idx);
+  p.k_scale = k_scale;
+  p.mass = mass;
+  p.to_kv = reinterpret_cast<uint8_t*>(dst_kv_cache);
+  p.to_k_idx = reinterpret_cast<uint8_t*>(dst_k_idx);
+  p.to_k_scale = dst_k_scale;
+  p.to_mass = dst_mass;
+  p.kept = kept;
+  p.new_lens = new_lens;
+  p.seqlens = g.seqlens;
+  p.table = g.block_table;
+  p.to_table = t.block_table;
+  p.mass_ld = mass_ld;
+  p.to_mass_ld = dst_mass_ld;
+  p.keep = keep;
+  p.in_place = !dst;
+  p.max_ctx = g.max_ctx, p.page_size = g.page_size, p.max_pages = g.max_pages;
+  p.num_pages = g.num_pages;
+  p.to_max_ctx = t.max_ctx, p.to_page_size = t.page_size, p.to_max_pages = t.max_pages;
+  p.to_num_pages = t.num_pages;
+  cache_compact_kernel<<<dim3((unsigned)g.batch, kCompactSlices), kCompactThreads, 0,
+                         (cudaStream_t)stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 from typing import Optional, Tuple
 
@@ -48,6 +49,15 @@ class QDescC(ctypes.Structure):
     _fields_ = [("num_q", ctypes.c_int32), ("q_per_seq", ctypes.c_int32),
                 ("row_begin", ctypes.c_int32), ("row_count", ctypes.c_int32),
                 ("q_start", ctypes.c_void_p)]
+
+
+class RopeDescC(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("rot_begin", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("num_rows", ctypes.c_int64), ("x_row_stride", ctypes.c_int64),
+                ("x_head_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -101,6 +111,23 @@ SIGNATURES = {
     "dsa_forward_fused": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.POINTER(KvDescC),
                                          ctypes.POINTER(QDescC), ctypes.c_int32, ctypes.c_float,
                                          ctypes.c_int32, _P, ctypes.c_size_t, _P, _P, _P, _P]),
+    "dsa_rope": (ctypes.c_int, [_P, _P, _P, ctypes.POINTER(RopeDescC), _P, _P]),
+    "dsa_rope_bwd": (ctypes.c_int, [_P, _P, _P, ctypes.POINTER(RopeDescC), _P, _P]),
+    "dsa_cache_append": (ctypes.c_int, [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P,
+                                        ctypes.c_float, ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.POINTER(KvDescC), ctypes.POINTER(QDescC), _P, _P,
+                                        _P, _P]),
+    "dsa_attn_mass_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(KvDescC),
+                                                       ctypes.POINTER(QDescC), ctypes.c_int32]),
+    "dsa_attn_mass": (ctypes.c_int, [_P, _P, ctypes.POINTER(KvDescC), ctypes.POINTER(QDescC), _P,
+                                     ctypes.c_int32, ctypes.c_float, _P, _P, ctypes.c_int64, _P,
+                                     ctypes.c_size_t, _P]),
+    "dsa_evict_select": (ctypes.c_int, [_P, ctypes.c_int64, ctypes.POINTER(KvDescC),
+                                        ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P,
+                                        _P]),
+    "dsa_cache_compact": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int64, ctypes.POINTER(KvDescC),
+                                         _P, ctypes.c_int32, _P, ctypes.POINTER(KvDescC), _P, _P,
+                                         _P, _P, ctypes.c_int64, _P]),
     "dsa_get_device_error": (ctypes.c_int, [_P]),
     "dsa_set_wait_timeout_ns": (ctypes.c_uint64, [ctypes.c_uint64]),
     "dsa_selftest_wait_timeout": (ctypes.c_int, [_P]),
@@ -503,6 +530,262 @@ def dsa_mha_prefill(q_idx, w, k_idx, k_scale, q_mha, kv_cache, w_uk, w_uv, kv: K
                                  workspace.numel(), _ptr(idx_out), _ptr(out), _ptr(lse),
                                  _stream(stream)), "dsa_mha_prefill")
     return out, lse, idx_out
+
+
+# ---- filling, weighing and trimming the two caches --------------------------------------
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_HALF, _INTERLEAVED, _NONE = 0, 1, 2
+D_ROPE = 64
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+               factor: float = 1.0, original_ctx: int = 4096, beta_fast: float = 32.0,
+               beta_slow: float = 1.0, device=None) -> Tuple[torch.Tensor, float]:
+    """Radians per position of each pair (fp64 [rot_dim / 2]) and the magnitude that goes
+    with them, for ``dsa_rope`` and ``dsa_cache_append``. With theta_i = base^(-2i / rot_dim):
+      None      theta_i
+      "linear"  theta_i / factor (position interpolation)
+      "ntk"     the same for base * factor^(rot_dim / (rot_dim - 2))
+      "yarn"    g_i theta_i + (1 - g_i) theta_i / factor, g_i rising linearly from 0 at
+                beta_slow to 1 at beta_fast turns over original_ctx positions, and the
+                magnitude 0.1 ln(factor) + 1 (YaRN, arXiv 2309.00071, section 3.2 and
+                equation 22)
+    Any other schedule is a tensor of one's own."""
+    if rot_dim < 2 or rot_dim % 2 or base <= 0 or factor <= 0 or original_ctx < 1:
+        raise ValueError("rope_freqs: rot_dim must be even and base, factor, original_ctx positive")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"rope_freqs: unknown scaling {scaling!r}")
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("rope_freqs: ntk scaling needs rot_dim >= 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2.0))
+    theta = [base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+    magnitude = 1.0
+    if scaling == "linear":
+        theta = [t / factor for t in theta]
+    elif scaling == "yarn":
+        if beta_fast <= beta_slow:
+            raise ValueError("rope_freqs: beta_fast must exceed beta_slow")
+        turns = [original_ctx * t / (2.0 * math.pi) for t in theta]
+        g = [min(1.0, max(0.0, (r - beta_slow) / (beta_fast - beta_slow))) for r in turns]
+        theta = [gi * t + (1.0 - gi) * t / factor for gi, t in zip(g, theta)]
+        magnitude = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+    return torch.tensor(theta, dtype=torch.float64, device=device), magnitude
+
+
+def _need(name: str, t: torch.Tensor, dtype, shape, device):
+    """A contiguous CUDA tensor of this type, shape and device (shape None: any)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return _ptr(t)
+
+
+def _cache_ptrs(kv: KvLayout, kv_cache, k_idx, k_scale, device):
+    """The three cache arrays of one geometry, checked."""
+    n = ((kv.num_pages, kv.page_size) if kv.paged else (kv.batch, kv.max_ctx))
+    return (_need("kv_cache", kv_cache, torch.bfloat16, (*n, D_QK), device),
+            _need("k_idx", k_idx, torch.uint8, (*n, D_IDX), device),
+            _need("k_scale", k_scale, torch.float32, n, device))
+
+
+class _Launch:
+    """The device of the call's tensors made current, and the stream of the call."""
+
+    def __init__(self, device: torch.device, stream):
+        if device.type != "cuda":
+            raise ValueError("tensors passed to the DSA library must be CUDA tensors")
+        self.other = None
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.other = torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *a):
+        if self.other is not None:
+            self.other.__exit__(*a)
+
+
+def _rope(where, x, positions, freqs, out, rot_begin, interleaved, magnitude, stream):
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [rows, dim] or [rows, heads, dim]")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    dev = x.device
+    with _Launch(dev, stream) as st:
+        if out is None:
+            if stream is not None:
+                with torch.cuda.stream(stream):
+                    out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            else:
+                out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
+            raise ValueError("out must have x's shape, type and device")
+        rows, dim = x.shape[0], x.shape[-1]
+        heads = x.shape[1] if x.dim() == 3 else 1
+        if dim > 1 and (x.stride(-1) != 1 or out.stride(-1) != 1):
+            raise ValueError("the last axis of x and out must be contiguous")
+        if freqs.dim() != 1:
+            raise ValueError("freqs must be one-dimensional")
+        d = RopeDescC(_DTYPES[x.dtype], _INTERLEAVED if interleaved else _HALF, heads, dim,
+                      rot_begin, 2 * freqs.shape[0], magnitude, rows, x.stride(0),
+                      x.stride(1) if x.dim() == 3 else dim, out.stride(0),
+                      out.stride(1) if x.dim() == 3 else dim)
+        if heads == 0 or rows == 0:
+            return out
+        _check(getattr(lib(), where)(
+            x.data_ptr(), _need("positions", positions, torch.int32, (rows,), dev),
+            _need("freqs", freqs, torch.float64, None, dev), ctypes.byref(d), out.data_ptr(), st),
+            where)
+    return out
+
+
+def dsa_rope(x, positions, freqs, out=None, rot_begin: int = 0, interleaved: bool = False,
+             magnitude: float = 1.0, stream=None) -> torch.Tensor:
+    """Rotary positions on dims [rot_begin, rot_begin + 2 len(freqs)) of every head of x
+    [rows, dim] or [rows, heads, dim] (strided views allowed); ``out=x`` works in place.
+    positions int32 [rows]; freqs, magnitude as ``rope_freqs`` gives them (include/dsa.h)."""
+    return _rope("dsa_rope", x, positions, freqs, out, rot_begin, interleaved, magnitude, stream)
+
+
+def dsa_rope_bwd(dout, positions, freqs, dx=None, rot_begin: int = 0, interleaved: bool = False,
+                 magnitude: float = 1.0, stream=None) -> torch.Tensor:
+    """The gradient of ``dsa_rope``'s input from that of its output; ``dx=dout`` works in
+    place. Where the forward read one row or head for several (a broadcast input), dx has
+    each one's part, to be summed."""
+    return _rope("dsa_rope_bwd", dout, positions, freqs, dx, rot_begin, interleaved, magnitude,
+                 stream)
+
+
+def dsa_cache_append(latent_new, k_new, kv_cache, k_idx, k_scale, kv: KvLayout, q_per_seq: int,
+                     freqs, positions=None, interleaved: bool = True,
+                     idx_interleaved: Optional[bool] = False, magnitude: float = 1.0, rows=None,
+                     stream=None, q_start=None) -> None:
+    """The new tokens into both caches (include/dsa.h): latent_new bf16 [T, 576] (the last
+    64 dims not yet rotated) and k_new bf16 [T, 128], each row's elements consecutive. Token
+    t goes to the slot of query row t; its rotary position is that slot, or positions[t].
+    ``interleaved`` is the pairing of the latent's rope dims, ``idx_interleaved`` that of the
+    key's first 64 dims (None: the key is not rotated)."""
+    T, dev = latent_new.shape[0], kv_cache.device
+    for name, x, dim in (("latent_new", latent_new, D_QK), ("k_new", k_new, D_IDX)):
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape != (T, dim) or x.device != dev:
+            raise ValueError(f"{name} must be a bfloat16 [T, {dim}] tensor on {dev}")
+        if x.stride(1) != 1:
+            raise ValueError(f"the last axis of {name} must be contiguous")
+    caches = _cache_ptrs(kv, kv_cache, k_idx, k_scale, dev)
+    kvd, qd = kv.c(), _qdesc(T, q_per_seq, rows, q_start)
+    with _Launch(dev, stream) as st:
+        _check(lib().dsa_cache_append(
+            latent_new.data_ptr(), latent_new.stride(0) if T > 1 else D_QK, k_new.data_ptr(),
+            k_new.stride(0) if T > 1 else D_IDX,
+            None if positions is None else _need("positions", positions, torch.int32, (T,), dev),
+            _need("freqs", freqs, torch.float64, (D_ROPE // 2,), dev), float(magnitude),
+            _INTERLEAVED if interleaved else _HALF,
+            _NONE if idx_interleaved is None else _INTERLEAVED if idx_interleaved else _HALF,
+            ctypes.byref(kvd), ctypes.byref(qd), *caches, st), "dsa_cache_append")
+
+
+def dsa_attn_mass_workspace_size(kv: KvLayout, num_q: int, q_per_seq: int, k: int, rows=None,
+                                 q_start=None) -> int:
+    kvd, qd = kv.c(), _qdesc(num_q, q_per_seq, rows, q_start)
+    return int(lib().dsa_attn_mass_workspace_size(ctypes.byref(kvd), ctypes.byref(qd), k))
+
+
+def _mass_ptr(name, mass, kv: KvLayout, dev):
+    if mass.dim() != 2 or mass.shape[0] != kv.batch or mass.shape[1] < kv.max_ctx:
+        raise ValueError(f"{name} must be [batch, >= max_ctx]")
+    return _need(name, mass, torch.float32, None, dev)
+
+
+def dsa_attn_mass(q, kv_cache, kv: KvLayout, q_per_seq: int, idx, scale: float, lse, mass,
+                  workspace: Optional[torch.Tensor] = None, rows=None, stream=None,
+                  q_start=None) -> torch.Tensor:
+    """The head mean of the window's attention weights added to mass [batch, >= max_ctx], by
+    slot (include/dsa.h): idx [T, k] and lse [T, 128] as the forward used and wrote them;
+    ``workspace`` is a 256-B aligned device tensor (a fresh one when None)."""
+    T, dev = q.shape[0], q.device
+    k = idx.shape[1]
+    kvd, qd = kv.c(), _qdesc(T, q_per_seq, rows, q_start)
+    args = (_need("q", q, torch.bfloat16, (T, HEADS, D_QK), dev),
+            _need("kv_cache", kv_cache, torch.bfloat16, None, dev), ctypes.byref(kvd),
+            ctypes.byref(qd), _need("idx", idx, torch.int32, (T, k), dev), k, float(scale),
+            _need("lse", lse, torch.float32, (T, HEADS), dev), _mass_ptr("mass", mass, kv, dev),
+            mass.shape[1])
+    with _Launch(dev, stream) as st:
+        if workspace is None:
+            n = max(256, int(lib().dsa_attn_mass_workspace_size(ctypes.byref(kvd),
+                                                                ctypes.byref(qd), k)))
+            if stream is not None:
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            else:
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        nbytes = workspace.numel() * workspace.element_size()
+        _check(lib().dsa_attn_mass(*args, _ptr(workspace), nbytes, st), "dsa_attn_mass")
+    return mass
+
+
+def dsa_evict_select(mass, kv: KvLayout, keep: int, sink: int = 0, recent: int = 0,
+                     kept: Optional[torch.Tensor] = None,
+                     new_lens: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The slots that stay when each sequence is trimmed to ``keep`` tokens (include/dsa.h):
+    (kept int32 [batch, keep] ascending and padded with -1, new_lens int32 [batch])."""
+    dev = mass.device
+    ptr = _mass_ptr("mass", mass, kv, dev)
+    kvd = kv.c()
+    with _Launch(dev, stream) as st:
+        if kept is None or new_lens is None:
+            with torch.cuda.stream(stream):  # None: the current stream
+                if kept is None:
+                    kept = torch.empty(kv.batch, max(keep, 0), dtype=torch.int32, device=dev)
+                if new_lens is None:
+                    new_lens = torch.empty(kv.batch, dtype=torch.int32, device=dev)
+        _check(lib().dsa_evict_select(
+            ptr, mass.shape[1], ctypes.byref(kvd), keep, sink, recent,
+            _need("kept", kept, torch.int32, (kv.batch, keep), dev),
+            _need("new_lens", new_lens, torch.int32, (kv.batch,), dev), st), "dsa_evict_select")
+    return kept, new_lens
+
+
+def dsa_cache_compact(kv_cache, k_idx, k_scale, kv: KvLayout, kept, new_lens,
+                      mass: Optional[torch.Tensor] = None, dst: Optional[KvLayout] = None,
+                      dst_kv_cache=None, dst_k_idx=None, dst_k_scale=None, dst_mass=None,
+                      stream=None) -> None:
+    """Moves the tokens that stay together (include/dsa.h), in place, or into the slots of
+    ``dst``: other cache arrays, or the same ones with pages that no source sequence uses."""
+    dev = kv_cache.device
+    src = _cache_ptrs(kv, kv_cache, k_idx, k_scale, dev)
+    kvd = kv.c()
+    if dst is None:
+        to, dstd, dst_batch = (dst_kv_cache, dst_k_idx, dst_k_scale), None, kv.batch
+        if any(t is not None for t in (*to, dst_mass)):
+            raise ValueError("dst arrays need a dst layout")
+    else:
+        to, dstd, dst_batch = _cache_ptrs(dst, dst_kv_cache, dst_k_idx, dst_k_scale, dev), \
+            ctypes.byref(dst.c()), dst.batch
+    if dst_batch != kv.batch:
+        raise ValueError("dst must have the source's batch")
+    if kept.dim() != 2 or kept.shape[0] != kv.batch:
+        raise ValueError("kept must be [batch, keep]")
+    if dst is not None and (mass is None) != (dst_mass is None):
+        raise ValueError("mass and dst_mass go together")
+    m = None if mass is None else _mass_ptr("mass", mass, kv, dev)
+    dm = None if dst_mass is None else _mass_ptr("dst_mass", dst_mass, dst, dev)
+    with _Launch(dev, stream) as st:
+        _check(lib().dsa_cache_compact(
+            *src, m, mass.shape[1] if mass is not None else 0, ctypes.byref(kvd),
+            _need("kept", kept, torch.int32, None, dev), kept.shape[1],
+            _need("new_lens", new_lens, torch.int32, (kv.batch,), dev), dstd, *to, dm,
+            dst_mass.shape[1] if dst_mass is not None else 0, st), "dsa_cache_compact")
 
 
 def dsa_get_device_error(stream=None) -> int:

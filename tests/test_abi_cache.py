@@ -1,0 +1,171 @@
+"""CPU checks of the calls around the caches: struct layout and the host-side refusals
+(nothing is launched: every call here fails its checks first)."""
+
+import ctypes
+import os
+import subprocess
+import tempfile
+
+import pytest
+import torch
+
+from sparse_attention_05_b200 import dsa
+from tests.test_abi import HEADER, _kv
+
+by = ctypes.byref
+FAKE = ctypes.c_void_p(0x100000)   # never dereferenced
+OTHER = ctypes.c_void_p(0x900000)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from sparse_attention_05_b200.build import build
+    build()
+    return dsa.lib()
+
+
+def test_rope_struct_layout_matches_c():
+    src = r"""
+    #include <stdio.h>
+    #include <stddef.h>
+    #include "dsa.h"
+    int main(void) {
+      printf("%zu %zu %zu %zu\n", sizeof(dsa_rope_desc_t), offsetof(dsa_rope_desc_t, magnitude),
+             offsetof(dsa_rope_desc_t, num_rows), offsetof(dsa_rope_desc_t, out_head_stride));
+      return 0;
+    }
+    """
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "l.c"), os.path.join(d, "l")
+        open(c, "w").write(src)
+        subprocess.run(["gcc", "-I", os.path.dirname(HEADER), c, "-o", exe], check=True)
+        got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True).stdout.split()]
+    D = dsa.RopeDescC
+    assert got == [ctypes.sizeof(D), D.magnitude.offset, D.num_rows.offset,
+                   D.out_head_stride.offset]
+
+
+def _rope(**kw):
+    d = dict(dtype=0, layout=1, heads=4, dim=96, rot_begin=32, rot_dim=64, magnitude=1.0,
+             num_rows=3, x_row_stride=384, x_head_stride=96, out_row_stride=384,
+             out_head_stride=96)
+    d.update(kw)
+    return dsa.RopeDescC(**d)
+
+
+def _call_rope(lib, d, x=FAKE, out=OTHER, pos=FAKE, f=FAKE):
+    a = lib.dsa_rope(x, pos, f, by(d), out, None)
+    assert a == lib.dsa_rope_bwd(x, pos, f, by(d), out, None)
+    return a
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(dtype=3), 1), (dict(layout=2), 1), (dict(heads=0), 1), (dict(dim=0), 1),
+    (dict(rot_dim=0), 1), (dict(rot_dim=63), 1), (dict(rot_begin=-1), 1), (dict(rot_begin=33), 1),
+    (dict(num_rows=-1), 1), (dict(magnitude=float("nan")), 1), (dict(magnitude=float("inf")), 1),
+    (dict(x_row_stride=-1), 1), (dict(num_rows=1 << 31), 2),
+    (dict(dim=1024, rot_begin=0, rot_dim=514, x_head_stride=1024, out_head_stride=1024), 2),
+    (dict(out_head_stride=95), 1),      # heads of the output overlap
+    (dict(out_head_stride=0), 1),
+    (dict(out_row_stride=383), 1),      # rows of the output overlap
+])
+def test_rope_refusals(lib, bad, status):
+    assert _call_rope(lib, _rope(**bad)) == status
+
+
+def test_rope_refuses_null_unaligned_and_overlapping(lib):
+    d = _rope()
+    assert _call_rope(lib, d, x=None) == 1 and _call_rope(lib, d, out=None) == 1
+    assert _call_rope(lib, d, pos=None) == 1 and _call_rope(lib, d, f=None) == 1
+    assert _call_rope(lib, d, x=ctypes.c_void_p(0x100001)) == 1
+    assert _call_rope(lib, d, f=ctypes.c_void_p(0x100004)) == 1
+    # out one head into x: neither in place nor apart
+    assert _call_rope(lib, d, out=ctypes.c_void_p(0x100000 + 96 * 2)) == 1
+    # the same start with other strides, and a broadcast input written over itself
+    assert _call_rope(lib, _rope(out_head_stride=128, out_row_stride=512), out=FAKE) == 1
+    assert _call_rope(lib, _rope(x_head_stride=0), out=FAKE) == 1
+    # no rows: nothing to do, whatever the pointers
+    assert _call_rope(lib, _rope(num_rows=0), x=None, out=None, pos=None, f=None) == 0
+
+
+def _append(lib, kv=None, q=None, lat=FAKE, ls=576, key=FAKE, ks=128, pos=None, f=FAKE, m=1.0,
+            ll=1, kl=0, kvc=FAKE, ki=FAKE, sc=FAKE):
+    return lib.dsa_cache_append(lat, ls, key, ks, pos, f, m, ll, kl, by(kv or _kv()),
+                                by(q or dsa.QDescC(2, 1, 0, 0)), kvc, ki, sc, None)
+
+
+def test_append_refusals(lib):
+    for name in ("lat", "key", "f", "kvc", "ki", "sc"):
+        assert _append(lib, **{name: None}) == 1, name
+    for name in ("lat", "key", "kvc", "ki"):
+        assert _append(lib, **{name: ctypes.c_void_p(0x100008)}) == 1, name
+    assert _append(lib, sc=ctypes.c_void_p(0x100002)) == 1
+    assert _append(lib, ls=568) == 1 and _append(lib, ls=580) == 1
+    assert _append(lib, ks=120) == 1 and _append(lib, ks=129) == 1
+    assert _append(lib, ll=2) == 1 and _append(lib, kl=3) == 1
+    assert _append(lib, m=float("nan")) == 1
+    assert _append(lib, q=dsa.QDescC(3, 1, 0, 0)) == 1
+    assert _append(lib, kv=_kv(layout=1, page=48, pages=4, max_pages=16, bt=0x2000)) == 2
+    # a ragged batch without a single new token
+    assert _append(lib, q=dsa.QDescC(0, 1, 0, 0, 0x3000), lat=None, key=None) == 0
+
+
+def _mass(lib, kv=None, q=None, qp=FAKE, kvc=FAKE, idx=FAKE, k=16, scale=0.04, lse=FAKE,
+          mass=FAKE, ld=512, ws=FAKE, nb=1 << 20):
+    return lib.dsa_attn_mass(qp, kvc, by(kv or _kv()), by(q or dsa.QDescC(2, 1, 0, 0)), idx, k,
+                             scale, lse, mass, ld, ws, nb, None)
+
+
+def test_attn_mass_refusals(lib):
+    for name in ("qp", "kvc", "idx", "lse", "mass"):
+        assert _mass(lib, **{name: None}) == 1, name
+    assert _mass(lib, k=0) == 2 and _mass(lib, k=(1 << 20) + 1) == 2
+    assert _mass(lib, scale=0.0) == 1 and _mass(lib, scale=float("nan")) == 1
+    assert _mass(lib, ld=511) == 1
+    assert _mass(lib, ws=None) == 6 and _mass(lib, ws=ctypes.c_void_p(0x100080)) == 6
+    assert _mass(lib, nb=100) == 6
+    assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(dsa.QDescC(2, 1, 0, 0)), 0) == 0
+    assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(dsa.QDescC(3, 1, 0, 0)), 16) == 0
+    assert _mass(lib, kv=_kv(batch=65536, max_ctx=16), q=dsa.QDescC(65536, 1, 0, 0), ld=16) == 2
+
+
+def test_evict_and_compact_refusals(lib):
+    kv = _kv()
+
+    def sel(mass=FAKE, ld=512, keep=8, sink=2, recent=3, kept=FAKE, lens=FAKE):
+        return lib.dsa_evict_select(mass, ld, by(kv), keep, sink, recent, kept, lens, None)
+    for name in ("mass", "kept", "lens"):
+        assert sel(**{name: None}) == 1, name
+    assert sel(ld=511) == 1 and sel(keep=0, sink=0, recent=0) == 1
+    assert sel(sink=-1) == 1 and sel(recent=-1) == 1 and sel(keep=4) == 1
+
+    def com(a=FAKE, b=FAKE, c=FAKE, mass=FAKE, ld=512, kept=FAKE, keep=8, lens=FAKE, dst=None,
+            ta=None, tb=None, tc=None, tm=None, tld=0):
+        return lib.dsa_cache_compact(a, b, c, mass, ld, by(kv), kept, keep, lens,
+                                     by(dst) if dst else None, ta, tb, tc, tm, tld, None)
+    for name in ("a", "b", "c", "kept", "lens"):
+        assert com(**{name: None}) == 1, name
+    assert com(keep=0) == 1 and com(ld=511) == 1
+    assert com(ta=FAKE) == 1                      # destination arrays without a geometry
+    to = dict(dst=_kv(max_ctx=64), ta=OTHER, tb=OTHER, tc=OTHER, tm=OTHER, tld=64)
+    assert com(**dict(to, tb=None)) == 1
+    assert com(**dict(to, tm=None)) == 1          # mass without a place for it
+    assert com(**dict(to, tld=63)) == 1
+    assert com(**dict(to, dst=_kv(batch=3, max_ctx=64))) == 1
+    assert com(**dict(to, dst=_kv(layout=1, page=32, pages=4, max_pages=16, bt=0x2000))) == 2
+
+
+def test_binding_refuses_wrong_tensors():
+    """Types, shapes and devices the pointers alone would not show."""
+    x = torch.zeros(2, 4, 64)
+    with pytest.raises(ValueError):
+        dsa.dsa_rope(x, torch.zeros(2, dtype=torch.int32), torch.zeros(32, dtype=torch.float64))
+    with pytest.raises(ValueError):
+        dsa.dsa_rope(torch.zeros(4), None, None)
+    with pytest.raises(ValueError):
+        dsa.dsa_rope(x.double(), None, None)
+    kv = dsa.KvLayout(2, 64)
+    with pytest.raises(ValueError):
+        dsa.dsa_evict_select(torch.zeros(2, 63), kv, 8)
+    with pytest.raises(ValueError):
+        dsa.dsa_evict_select(torch.zeros(2, 64), kv, 8)  # not on a GPU

@@ -1,0 +1,199 @@
+"""GPU parity of dsa_attn_mass against the fp64 oracle.
+
+Tolerance per listed entry. A logit z = scale q.c: the tensor core sums 576 products in
+fp32, off by at most 2 * 576 * 2^-24 sum |q_d c_d| scale (the order and inner rounding of the
+sum are not specified, hence the 2); scale, log2 e and the LSE are rounded once each and the
+difference once more: (|z| + |lse|) * 2^-22. A head's weight a is off by a times that, plus
+2^-21 a for the exponential; the head sum adds 128 roundings of 2^-24, the mean two. With many
+rows a weight is rounded to 2^-41. The sum into fp32 mass adds half a step (2^-24) per row."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import attn_weight, resolve_kv_rows, sparse_mla
+from sparse_attention_05_b200 import dsa, synth
+from tests.helpers import oracle_args
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _reference(a, T, q_seq, q_pos, idx, lse, scale, mass0, rows, bt, page):
+    mass = mass0.astype(np.float64).copy()
+    tol = np.zeros_like(mass)
+    count = np.zeros_like(mass)
+    for t in rows:
+        b, pos = int(q_seq[t]), int(q_pos[t])
+        sel = [int(s) for s in idx[t] if 0 <= s <= pos]
+        if not sel:
+            continue
+        c = np.asarray(resolve_kv_rows(a["kv"], b, sel, bt, page), np.float64)
+        q = np.asarray(a["q"][t], np.float64)
+        p, terms = attn_weight(q, c, scale, lse[t])
+        z = np.abs(scale * (q @ c.T))
+        dz = 2 * 576 * 2.0 ** -24 * scale * (np.abs(q) @ np.abs(c).T) + \
+            (z + np.abs(lse[t])[:, None]) * 2.0 ** -22 + 2.0 ** -21
+        e = (terms * np.expm1(dz)).mean(0) + p * 130 * 2.0 ** -24 + 2.0 ** -41
+        for s, v, w in zip(sel, p, e):
+            mass[b, s] += v
+            tol[b, s] += w
+            count[b, s] += 1
+    tol += (count + 1) * 2.0 ** -24 * np.abs(mass)
+    return mass, tol
+
+
+def _lists(T, q_pos, k, seed, dup=False):
+    r = np.random.default_rng(seed)
+    idx = np.full((T, k), -1, np.int32)
+    for t in range(T):
+        n = min(k, int(q_pos[t]) + 1)
+        idx[t, :n] = np.sort(r.permutation(int(q_pos[t]) + 1)[:n])
+    return idx
+
+
+def _check(p, idx, window=None, seed=0, workspace=None):
+    a = oracle_args(p)
+    T = p.num_q
+    q_seq, q_pos = a["q_seq"], a["q_pos"]
+    lens = p.q_lens().numpy()
+    start = np.concatenate([[0], np.cumsum(lens)])
+    w0, wc = window if window else (0, 0)
+    rows = [t for t in range(T) if w0 <= t - start[q_seq[t]] and
+            (not wc or t - start[q_seq[t]] < w0 + wc)]
+    _, lse = sparse_mla(a["q"], a["kv"], q_seq, q_pos, idx, p.scale, 512,
+                        block_table=a["block_table"], page_size=p.page_size)
+    lse = lse.astype(np.float32)
+    mass0 = np.random.default_rng(seed).random((p.batch, p.max_ctx + 5)).astype(np.float32)
+    g = p.to(DEV)
+    mass = torch.from_numpy(mass0).cuda()
+    args = (g.q, g.kv, dsa.KvLayout.of(g), p.q_per_seq, torch.from_numpy(idx).cuda(), p.scale,
+            torch.from_numpy(lse).cuda())
+    got = dsa.dsa_attn_mass(*args, mass, workspace, rows=window, q_start=g.q_start)
+    torch.cuda.synchronize()
+    assert dsa.dsa_get_device_error() == 0 and got is mass
+    ref, tol = _reference(a, T, q_seq, q_pos, idx, lse, p.scale, mass0, rows, a["block_table"],
+                          p.page_size)
+    err = np.abs(mass.double().cpu().numpy() - ref)
+    assert np.all(err <= tol), f"max excess {np.max(err - tol):.3e}, max err {err.max():.3e}"
+    assert np.array_equal(mass.cpu().numpy()[tol == 0], mass0[tol == 0])
+    # the same bits again
+    again = torch.from_numpy(mass0).cuda()
+    dsa.dsa_attn_mass(*args, again, rows=window, q_start=g.q_start)
+    assert torch.equal(again, mass)
+    return mass0, mass
+
+
+def _idx(p, k, seed):
+    return _lists(p.num_q, oracle_args(p)["q_pos"], k, seed)
+
+
+@pytest.mark.parametrize("k", [1, 100, 128, 129, 700])
+def test_decode(k):
+    p = synth.decode(batch=3, ctx=900, q_per_seq=1, seed=70 + k)
+    mass0, mass = _check(p, _idx(p, k, k))
+    # every row spreads a weight of one: 900 roundings of 2^-24 in the difference
+    spread = (mass.double().cpu().numpy() - mass0).sum(1)
+    assert np.all(np.abs(spread - 1) <= 1e-3)
+
+
+def test_paged_two_rows_and_short_context():
+    p = synth.paged_decode(batch=4, q_per_seq=2, min_ctx=3, max_ctx=700, page_size=64, seed=81)
+    _check(p, _idx(p, 256, 1))
+
+
+@pytest.mark.parametrize("rows", [8, 9, 40])
+def test_few_and_many_rows_of_a_sequence(rows):
+    """On both sides of the border between the two ways of summing."""
+    p = synth.ragged([300, 200], [rows, rows // 2], seed=82 + rows)
+    _check(p, _idx(p, 150, rows))
+
+
+def test_ragged_rows_with_an_empty_sequence_and_a_window():
+    p = synth.ragged([400, 50, 130], [30, 0, 12], seed=83)
+    idx = _idx(p, 64, 3)
+    _check(p, idx)
+    _check(p, idx, window=(3, 5))
+    _check(p, idx, window=(1, 0))
+
+
+def test_listed_as_it_comes():
+    """Unordered lists, padding in the middle, entries past the row's position, the same
+    entry twice (it counts twice), a row without any entry."""
+    p = synth.decode(batch=4, ctx=300, q_per_seq=1, seed=84)
+    r = np.random.default_rng(5)
+    idx = r.integers(-3, 330, size=(4, 200)).astype(np.int32)
+    idx[1] = -1
+    idx[2, :100] = 7
+    _check(p, idx)
+
+
+def test_prefill_rows_shorter_than_the_list():
+    p = synth.prefill(L=200, seed=85)
+    _check(p, _idx(p, 128, 6))
+
+
+def test_nan_only_where_it_is_listed():
+    p = synth.decode(batch=2, ctx=200, q_per_seq=1, seed=86)
+    idx = _idx(p, 50, 7)
+    free = sorted(set(range(200)) - set(idx[0].tolist()))
+    for rows, T in ((1, 2), (10, 20)):
+        g = p.to(DEV)
+        q = g.q if rows == 1 else g.q.repeat_interleave(rows, 0)
+        li = np.repeat(idx, rows, 0)
+        lse = torch.zeros(T, 128, device=DEV)
+        kv = g.kv.clone()
+        kv[0, free] = float("nan")               # not listed by any row
+        kv[1, int(idx[1, 0])] = float("nan")     # listed
+        mass = torch.zeros(2, 200, device=DEV)
+        lay = dsa.KvLayout(2, 200, torch.tensor([200, 200], dtype=torch.int32, device=DEV))
+        dsa.dsa_attn_mass(q, kv, lay, rows, torch.from_numpy(li).cuda(), p.scale, lse + 3.0, mass)
+        assert dsa.dsa_get_device_error() == 0
+        bad = torch.isnan(mass).nonzero().cpu().tolist()
+        assert bad == [[1, int(idx[1, 0])]]
+
+
+def test_bad_page_and_bad_rows_are_reported():
+    p = synth.paged_decode(batch=3, q_per_seq=2, min_ctx=200, max_ctx=256, page_size=64, seed=87)
+    idx = _idx(p, 100, 8)
+    g = p.to(DEV)
+    lse = torch.zeros(6, 128, device=DEV)
+    mass = torch.zeros(3, 256, device=DEV)
+    lay = dsa.KvLayout.of(g)
+    lay.block_table = lay.block_table.clone()
+    lay.block_table[1, 0] = 1 << 20
+    dsa.dsa_attn_mass(g.q, g.kv, lay, 2, torch.from_numpy(idx).cuda(), p.scale, lse, mass)
+    assert dsa.dsa_get_device_error() == 5
+    lay = dsa.KvLayout.of(g)
+    lay.seqlens = lay.seqlens.clone()
+    lay.seqlens[2] = 1                            # shorter than its two rows
+    mass.zero_()
+    dsa.dsa_attn_mass(g.q, g.kv, lay, 2, torch.from_numpy(idx).cuda(), p.scale, lse, mass)
+    assert dsa.dsa_get_device_error() == 5
+    assert torch.all(mass[2] == 0) and torch.any(mass[0] != 0)
+
+
+def test_own_workspace_other_stream_and_graph():
+    p = synth.decode(batch=2, ctx=400, q_per_seq=1, seed=88)
+    idx = _idx(p, 200, 9)
+    n = dsa.dsa_attn_mass_workspace_size(dsa.KvLayout(2, 400), 2, 1, 200)
+    _check(p, idx, workspace=torch.empty(n, dtype=torch.uint8, device=DEV))
+    g = p.to(DEV)
+    for rows in (1, 12):
+        q = g.q.repeat_interleave(rows, 0)
+        li = torch.from_numpy(np.repeat(idx, rows, 0)).cuda()
+        lse = torch.full((2 * rows, 128), 6.0, device=DEV)
+        lay = dsa.KvLayout(2, 400, g.seqlens)
+        want = dsa.dsa_attn_mass(q, g.kv, lay, rows, li, p.scale, lse, torch.zeros(2, 400, device=DEV))
+        s = torch.cuda.Stream()
+        mass = torch.zeros(2, 400, device=DEV)
+        s.wait_stream(torch.cuda.current_stream())
+        dsa.dsa_attn_mass(q, g.kv, lay, rows, li, p.scale, lse, mass, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(mass, want)
+        graph = torch.cuda.CUDAGraph()
+        mass.zero_()
+        with torch.cuda.graph(graph):
+            dsa.dsa_attn_mass(q, g.kv, lay, rows, li, p.scale, lse, mass)
+        graph.replay()
+        assert torch.equal(mass, want)

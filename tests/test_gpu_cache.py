@@ -1,0 +1,325 @@
+"""GPU parity of dsa_cache_append, dsa_evict_select and dsa_cache_compact.
+
+Append tolerances: latent dims that pass through and keys that are not rotated are exact
+(bits and codes). A rotated value is within 2^-21 (|a| + |b|) m of the formula's (see
+test_gpu_rope), so its bf16 value within that and half a step, 2^-8 relative;
+the key's scale, amax / 448, within 2^-21 * 2 amax' / 448 + 2^-23 relative; a code's value
+within half an E4M3 step of the key: 2^-4 relative, 2^-10 scales below the normal range,
+widened by the 2^-20 by which key and scale may be off. Selections and moves are exact."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import append_token, bf16_round, cache_at, e4m3_decode, evict_select, key_codes
+from sparse_attention_05_b200 import dsa
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _caches(batch, ctx, paged, page=64, seed=0, extra=1):
+    """Cache arrays with recognisable contents, and their layout."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    if paged:
+        per = -(-ctx // page)
+        n = batch * per + extra
+        table = torch.randperm(n, generator=g, device=DEV)[:batch * per].int().view(batch, per)
+        shape = (n, page)
+    else:
+        table, shape, n = None, (batch, ctx), 0
+    kv = torch.randn(*shape, 576, generator=g, device=DEV).bfloat16()
+    codes = torch.randint(0, 256, (*shape, 128), generator=g, device=DEV, dtype=torch.uint8)
+    scale = torch.rand(*shape, generator=g, device=DEV)
+
+    def layout(lens):
+        if not paged:
+            return dsa.KvLayout(batch, ctx, lens)
+        return dsa.KvLayout(batch, ctx, lens, table, page, n)
+    return kv, codes, scale, table, layout
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def _check_append(lens, q_lens, ctx, paged, ragged, page=64, positions=None, interleaved=True,
+                  idx_interleaved=False, m=1.25, window=None, seed=1):
+    batch, T = len(lens), sum(q_lens)
+    kv, codes, scale, table, layout = _caches(batch, ctx, paged, page, seed)
+    g = torch.Generator(device=DEV).manual_seed(seed + 100)
+    lat = torch.randn(T, 640, generator=g, device=DEV).bfloat16()[:, 64:]
+    key = (torch.randn(T, 136, generator=g, device=DEV) * 3).bfloat16()[:, 8:]
+    f, _ = dsa.rope_freqs(64, device=DEV)
+    pos = None if positions is None else positions(T)
+    before = [t.clone() for t in (kv, codes, scale)]
+    start = np.concatenate([[0], np.cumsum(q_lens)])
+    dsa.dsa_cache_append(lat, key, kv, codes, scale, layout(_i32(lens)), max(q_lens), f, pos,
+                         interleaved=interleaved, idx_interleaved=idx_interleaved, magnitude=m,
+                         rows=window, q_start=_i32(start.tolist()) if ragged else None)
+    torch.cuda.synchronize()
+    assert dsa.dsa_get_device_error() == 0
+    tb = None if table is None else table.cpu().numpy()
+    fn = f.cpu().numpy()
+    got = [t.float().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
+           for t in (kv, codes, scale)]
+    old = [t.float().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
+           for t in before]
+    latn, keyn = lat.double().cpu().numpy(), key.double().cpu().numpy()
+    for b in range(batch):
+        for i in range(q_lens[b]):
+            if window and not window[0] <= i < window[0] + (window[1] or max(q_lens)):
+                continue
+            t, slot = start[b] + i, lens[b] - q_lens[b] + i
+            at = cache_at(b, slot, tb, page)
+            p = slot if pos is None else int(pos[t])
+            y, k, s = append_token(latn[t], keyn[t], p, fn, m, interleaved=interleaved,
+                                   idx_interleaved=idx_interleaved)
+            row = got[0][at]
+            assert np.array_equal(row[:512], latn[t][:512])
+            pair = np.abs(latn[t][512:]).max() * 2 * m * 2.0 ** -21
+            assert np.all(np.abs(row[512:] - y[512:]) <= pair * 1.01 + np.abs(y[512:]) * 2.0 ** -8)
+            gs, gc = got[2][at], got[1][at]
+            if idx_interleaved is None:
+                assert gs == s and np.array_equal(gc, key_codes(k.astype(np.float32), s))
+            else:
+                off = 2 * np.abs(keyn[t]).max() * m * 2.0 ** -21
+                assert abs(gs - float(s)) <= off / 448 + float(s) * 2.0 ** -23
+                v = e4m3_decode(gc).astype(np.float64) * gs
+                assert np.all(np.abs(v - k) <= np.abs(k) * 2.0 ** -4 * (1 + 2.0 ** -18)
+                              + gs * 2.0 ** -10 * (1 + 2.0 ** -18) + 2 * off)
+                # the dims that are not rotated: the codes for the scale it wrote
+                assert np.array_equal(gc[64:], key_codes(keyn[t][64:].astype(np.float32), gs))
+            for a, o in zip(got, old):
+                a[at] = o[at]
+    for a, o in zip(got, old):   # every other row is as it was
+        assert np.array_equal(a, o)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("interleaved,idx_interleaved", [(True, False), (False, True), (True, None)])
+def test_append_decode(paged, interleaved, idx_interleaved):
+    """Two tokens of each sequence; one pair ends and starts a page, one fills the cache."""
+    _check_append([2, 65, 200, 131], [2] * 4, 200, paged, False, interleaved=interleaved,
+                  idx_interleaved=idx_interleaved)
+
+
+def test_append_ragged_with_positions_and_empty_rows():
+    _check_append([70, 5, 300, 1], [70, 0, 33, 1], 300, True, True, page=128,
+                  positions=lambda T: torch.arange(T, device=DEV, dtype=torch.int32) * 9001 - 50)
+
+
+def test_append_window_of_rows():
+    _check_append([40, 60], [20, 20], 64, False, False, window=(5, 7))
+    _check_append([40, 60, 9], [20, 3, 0], 64, True, True, window=(2, 0), seed=5)
+
+
+def test_append_special_keys():
+    """A zero key, a NaN, an infinity: floor scale, NaN codes and scale, saturation."""
+    kv, codes, scale, _, layout = _caches(1, 8, False)
+    lat = torch.zeros(3, 576, device=DEV, dtype=torch.bfloat16)
+    key = torch.zeros(3, 128, device=DEV, dtype=torch.bfloat16)
+    key[1, 100], key[2, 70], key[2, 3] = float("nan"), float("inf"), 1.0
+    f, _ = dsa.rope_freqs(64, device=DEV)
+    dsa.dsa_cache_append(lat, key, kv, codes, scale, layout(_i32([3])), 3, f)
+    assert float(scale[0, 0]) == float(np.float32(2.0 ** -120) / np.float32(448))
+    assert torch.all(codes[0, 0] == 0)
+    assert torch.isnan(scale[0, 1]) and torch.all(codes[0, 1] & 0x7F == 0x7F)
+    assert torch.isinf(scale[0, 2]) and int(codes[0, 2, 70]) & 0x7F == 0x7F
+    assert torch.all(codes[0, 2, 71:] == 0)
+
+
+def test_append_reports_bad_pages_and_rows():
+    """The token of a page outside the cache and of a sequence shorter than its rows are
+    skipped and reported; the others are written."""
+    kv, codes, scale, table, layout = _caches(3, 128, True)
+    before = kv.clone()
+    f, _ = dsa.rope_freqs(64, device=DEV)
+    lat = torch.ones(6, 576, device=DEV, dtype=torch.bfloat16)
+    key = torch.ones(6, 128, device=DEV, dtype=torch.bfloat16)
+    good = table[0].clone()
+    table[1, 1] = 1 << 20
+    dsa.dsa_cache_append(lat, key, kv, codes, scale, layout(_i32([70, 66, 1])), 2, f)
+    torch.cuda.synchronize()
+    assert dsa.dsa_get_device_error() == 5
+    changed = (kv != before).any(-1).nonzero().cpu().tolist()
+    assert changed == [[int(good[1]), 4], [int(good[1]), 5]]
+    table[1, 1] = -1
+    dsa.dsa_cache_append(lat, key, kv, codes, scale, layout(_i32([70, 66, 66])), 2, f)
+    assert dsa.dsa_get_device_error() == 5
+
+
+# ---- selection -----------------------------------------------------------------------
+
+
+def _check_select(mass, lens, keep, sink, recent):
+    batch, ctx = mass.shape
+    kept, new = dsa.dsa_evict_select(mass, dsa.KvLayout(batch, ctx - 3, _i32(lens)), keep, sink,
+                                     recent)
+    torch.cuda.synchronize()
+    assert dsa.dsa_get_device_error() == 0
+    m, k = mass.cpu().numpy(), kept.cpu().numpy()
+    for b, n in enumerate(lens):
+        want = evict_select(m[b], n, keep, sink, recent)
+        assert int(new[b]) == len(want)
+        assert k[b].tolist() == want + [-1] * (keep - len(want)), f"sequence {b}"
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal", "special"])
+@pytest.mark.parametrize("ctx,keep,sink,recent", [
+    (40, 1, 0, 0), (1000, 500, 4, 64), (5000, 37, 0, 0), (5000, 4990, 1, 2), (3000, 100, 60, 40),
+    (70001, 20000, 16, 3000),
+])
+def test_select_against_a_sort(kind, ctx, keep, sink, recent):
+    g = torch.Generator(device=DEV).manual_seed(ctx + keep)
+    lens = [0, 1, keep, keep + 1, ctx - 7, ctx]
+    lens = [min(n, ctx) for n in lens]
+    m = torch.rand(len(lens), ctx + 3, generator=g, device=DEV)
+    if kind == "spread":
+        m = torch.exp((m - 0.5) * 60) * torch.where(m > 0.5, 1.0, -1.0)
+    elif kind == "ties":
+        m = (m * 5).round()
+    elif kind == "equal":
+        m = torch.zeros_like(m)
+    else:
+        v = torch.tensor([float("nan"), -float("inf"), float("inf"), 0.0, -0.0, 1e-45, -1.0],
+                         device=DEV)
+        m = v[(m * 6.99).long()]
+    _check_select(m.contiguous(), lens, keep, sink, recent)
+
+
+def test_select_reports_a_length_out_of_range():
+    m = torch.rand(3, 100, device=DEV)
+    kept, new = dsa.dsa_evict_select(m, dsa.KvLayout(3, 100, _i32([101, -1, 90])), 10)
+    assert dsa.dsa_get_device_error() == 5
+    assert new.tolist() == [0, 0, 10] and torch.all(kept[:2] == -1)
+
+
+# ---- compaction ----------------------------------------------------------------------
+
+
+def _lists(lens, keep, seed):
+    """Random kept lists: an unmoved beginning, gaps, the last slot."""
+    r = np.random.default_rng(seed)
+    kept = np.full((len(lens), keep), -1, np.int32)
+    new = []
+    for b, n in enumerate(lens):
+        k = min(n, keep)
+        s = np.sort(r.permutation(n)[:k]) if b % 2 == 0 or n == 0 else np.r_[
+            np.arange(k // 2), np.sort(r.permutation(np.arange(k // 2, n))[:k - k // 2])]
+        kept[b, :k] = s
+        new.append(k)
+    return torch.from_numpy(kept).cuda(), _i32(new)
+
+
+def _rows(cache, table, page, b, slots):
+    if table is None:
+        return cache[b, slots]
+    s = torch.as_tensor(slots, device=DEV)
+    return cache[table[b].long()[s // page], s % page]
+
+
+@pytest.mark.parametrize("paged,page", [(False, 64), (True, 64), (True, 128)])
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("lens,keep", [([9], 4), ([0, 1, 700, 333, 700], 300), ([5000, 4100], 2600),
+                                       ([12345], 9001)])
+def test_compact_moves_every_bit(paged, page, in_place, lens, keep):
+    ctx = max(lens) + 5
+    kv, codes, scale, table, layout = _caches(len(lens), ctx, paged, page, seed=keep)
+    mass = torch.rand(len(lens), ctx + 11, device=DEV)
+    kept, new = _lists(lens, keep, keep)
+    src = [t.clone() for t in (kv, codes, scale, mass)]
+    if in_place:
+        tkv, tcodes, tscale, ttable, tmass, tctx = kv, codes, scale, table, mass, ctx
+        want = [t.clone() for t in src]
+        dsa.dsa_cache_compact(kv, codes, scale, layout(_i32(lens)), kept, new, mass=mass)
+    else:
+        tkv, tcodes, tscale, ttable, tlayout = _caches(len(lens), keep, paged, page, seed=3)
+        tmass, tctx = torch.rand(len(lens), keep + 2, device=DEV), keep
+        want = [t.clone() for t in (tkv, tcodes, tscale, tmass)]
+        dsa.dsa_cache_compact(kv, codes, scale, layout(_i32(lens)), kept, new, mass=mass,
+                              dst=tlayout(None), dst_kv_cache=tkv, dst_k_idx=tcodes,
+                              dst_k_scale=tscale, dst_mass=tmass)
+        for a, b in zip((kv, codes, scale, mass), src):
+            assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    assert dsa.dsa_get_device_error() == 0
+    for b, n in enumerate(lens):
+        k = int(new[b])
+        s = kept[b, :k].long()
+        for w, x in zip(want[:3], src[:3]):
+            v = _rows(x, table, page, b, s)
+            i = torch.arange(k, device=DEV)
+            if ttable is None:
+                w[b, :k] = v
+            else:
+                w[ttable[b].long()[i // page], i % page] = v
+        want[3][b, k:min(n, tctx)] = 0
+        want[3][b, :k] = src[3][b, s]
+    for a, w in zip((tkv, tcodes, tscale, tmass), want):
+        assert torch.equal(a, w)
+
+
+def test_compact_into_fresh_pages_of_the_same_cache_without_mass():
+    kv, codes, scale, table, layout = _caches(2, 300, True, 64, seed=9, extra=6)
+    used = set(table.flatten().tolist())
+    free = torch.tensor([p for p in range(kv.shape[0]) if p not in used][:4], device=DEV)
+    to = dsa.KvLayout(2, 128, None, free.int().view(2, 2), 64, kv.shape[0])
+    kept, new = _lists([300, 250], 128, 4)
+    want = [torch.stack([_rows(x, table, 64, b, kept[b].long()) for b in range(2)])
+            for x in (kv, codes, scale)]
+    dsa.dsa_cache_compact(kv, codes, scale, layout(_i32([300, 250])), kept, new, dst=to,
+                          dst_kv_cache=kv, dst_k_idx=codes, dst_k_scale=scale)
+    for x, w in zip((kv, codes, scale), want):
+        assert torch.equal(x[free].reshape(2, 128, *x.shape[2:]), w)
+
+
+def test_compact_reports_bad_lists():
+    """Descending, repeated, too large and negative slots, lengths out of range: reported,
+    skipped, and the other sequences moved."""
+    kv, codes, scale, _, layout = _caches(4, 64, False)
+    before = kv.clone()
+    kept = _i32([[5, 4, 7, 8], [1, 1, 63, 64], [2, -1, 9, 10], [3, 9, 11, 13]])
+    dsa.dsa_cache_compact(kv, codes, scale, layout(_i32([64, 64, 64, 64])), kept, _i32([4, 4, 4, 4]))
+    assert dsa.dsa_get_device_error() == 5
+    assert torch.equal(kv[3, :4], before[3, [3, 9, 11, 13]])
+    assert torch.equal(kv[:, 4:], before[:, 4:])
+    for lens, new in (([64] * 4, [5, 4, 4, 4]), ([65, 64, 64, 64], [4] * 4), ([3, 64, 64, 64], [4] * 4),
+                      ([64] * 4, [-1, 4, 4, 4])):
+        kv.copy_(before)
+        good = _i32([[3, 9, 11, 13]] * 4)
+        dsa.dsa_cache_compact(kv, codes, scale, layout(_i32(lens)), good, _i32(new))
+        assert dsa.dsa_get_device_error() == 5
+        assert torch.equal(kv[0], before[0])
+        assert torch.equal(kv[1, :4], before[1, [3, 9, 11, 13]])
+
+
+def test_trimming_twice_and_captured():
+    """Select and compact captured into one graph and replayed: the second replay trims what
+    the first left (nothing moves any more)."""
+    kv, codes, scale, _, layout = _caches(3, 1000, False)
+    mass = torch.rand(3, 1000, device=DEV)
+    lens = _i32([1000, 640, 100])
+    lay = layout(lens)
+    kept = torch.empty(3, 200, dtype=torch.int32, device=DEV)
+    new = torch.empty(3, dtype=torch.int32, device=DEV)
+    start = [t.clone() for t in (kv, codes, scale, mass)]
+    graph = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        dsa.dsa_evict_select(mass, lay, 200, 4, 32, kept, new, stream=s)
+        dsa.dsa_cache_compact(kv, codes, scale, lay, kept, new, mass=mass, stream=s)
+        lens.copy_(new)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert lens.tolist() == [200, 200, 100]
+    after = [t.clone() for t in (kv, codes, scale, mass)]
+    for b, n in enumerate((1000, 640, 100)):
+        want = evict_select(start[3][b].cpu().numpy(), n, 200, 4, 32)
+        assert torch.equal(kv[b, :len(want)], start[0][b, want])
+        assert torch.equal(mass[b, :len(want)], start[3][b, want])
+    assert torch.all(mass[0, 200:] == 0) and torch.all(mass[1, 200:640] == 0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, w in zip((kv, codes, scale, mass), after):
+        assert torch.equal(a, w)
