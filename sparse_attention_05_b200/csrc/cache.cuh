@@ -107,13 +107,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
 
 // ---- compact ---------------------------------------------------------------------------
 // Moving in place: kept is ascending, so kept[i] >= i, and a chunk's destinations lie
-// below every later chunk's sources. One CTA takes a column slice of a sequence through
-// its chunks in order: it loads a chunk, waits for all its threads, and stores it. The
-// slices are independent of each other, which is where the parallelism comes from: nine
-// of 128 B of the latent row, one of the key row, one of scale and mass.
+// below every later chunk's sources. A cluster of CTAs takes a column slice of a sequence
+// through its chunks in order: it loads a chunk into shared memory, waits at the cluster's
+// barrier until all its CTAs have theirs, and stores it; the next chunk's loads are issued
+// before that wait. The slices are independent of each other: nine of 128 B of the latent
+// row, one of the key row, one of scale and mass. Into other pages the chunks need no
+// order, and plain CTAs take them.
 constexpr int kCompactThreads = 256;
 constexpr int kCompactSlices = 11;
-constexpr int kCompactUnroll = 4;
+constexpr int kCompactRows = kCompactThreads;            // rows of a CTA's chunk
+constexpr int kCompactSmemBytes = 2 * kCompactRows * 128;
 
 struct CompactParams {
   const uint8_t* kv;
@@ -130,22 +133,25 @@ struct CompactParams {
   const int32_t* table;        // paged source
   const int32_t* to_table;     // paged destination
   int64_t mass_ld, to_mass_ld;
-  int32_t keep, in_place;
+  int32_t keep, splits;        // splits: CTAs (the cluster's, in place) of one slice
   int32_t max_ctx, page_size, max_pages, num_pages;
   int32_t to_max_ctx, to_page_size, to_max_pages, to_num_pages;
 };
 
 // Row of the cache arrays that holds a slot, -1 for a page outside the cache.
-__device__ __forceinline__ int64_t cache_row(const int32_t* table, int b, int slot, int max_ctx,
-                                             int page_size, int max_pages, int num_pages) {
-  if (!table) return (int64_t)b * max_ctx + slot;
+__device__ __forceinline__ int cache_row(const int32_t* table, int b, int slot, int max_ctx,
+                                         int page_size, int max_pages, int num_pages) {
+  if (!table) return b * max_ctx + slot;
   const int pg = __ldg(table + (int64_t)b * max_pages + slot / page_size);
   if (pg < 0 || pg >= num_pages) return -1;
-  return (int64_t)pg * page_size + slot % page_size;
+  return pg * page_size + slot % page_size;
 }
 
+template <bool kInPlace>
 __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const CompactParams p) {
-  const int b = blockIdx.x, slice = blockIdx.y, tid = threadIdx.x;
+  extern __shared__ uint4 compact_smem[];
+  const int b = blockIdx.x / p.splits, rank = blockIdx.x % p.splits;
+  const int slice = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int len = p.seqlens ? __ldg(p.seqlens + b) : p.max_ctx;
   const int n = __ldg(p.new_lens + b);
   if (len < 0 || len > p.max_ctx || n < 0 || n > p.keep || n > len || n > p.to_max_ctx) {
@@ -153,66 +159,93 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
     return;
   }
   const int32_t* kept = p.kept + (int64_t)b * p.keep;
-  // the source and destination row of entry i, both -1 where the entry is out of range
-  auto rows_of = [&](int i, int64_t& src, int64_t& dst, int& slot) {
-    src = dst = -1;
-    if (i >= n) return;
+  const int step = p.splits * kCompactRows;
+  // this lane's entry of chunk c, whose row its warp moves
+  auto entry = [&](int c) { return c * step + rank * kCompactRows + tid; };
+  // its source row; -1: none, or already in its place
+  auto source = [&](int i, int& slot) {
+    if (i >= n) return -1;
     slot = __ldg(kept + i);
     bool ok = slot >= 0 && slot < len;
-    if (p.in_place) ok = ok && slot >= i && (i == 0 || slot > __ldg(kept + i - 1));
-    if (ok) {
-      src = cache_row(p.table, b, slot, p.max_ctx, p.page_size, p.max_pages, p.num_pages);
-      dst = cache_row(p.to_table, b, i, p.to_max_ctx, p.to_page_size, p.to_max_pages,
-                      p.to_num_pages);
+    if (kInPlace) {
+      ok = ok && slot >= i && (i == 0 || slot > __ldg(kept + i - 1));
+      if (ok && slot == i) return -1;
     }
-    if (src < 0 || dst < 0) {
-      report_error(kErrBounds);
-      src = dst = -1;
-    }
+    const int row = ok ? cache_row(p.table, b, slot, p.max_ctx, p.page_size, p.max_pages,
+                                   p.num_pages) : -1;
+    if (row < 0) report_error(kErrBounds);
+    return row;
   };
-  if (slice < 10) {  // 128 B a row, eight threads a row
-    const int piece = tid & 7;
+  auto destination = [&](int i) {
+    const int row = cache_row(p.to_table, b, i, p.to_max_ctx, p.to_page_size, p.to_max_pages,
+                              p.to_num_pages);
+    if (row < 0) report_error(kErrBounds);
+    return row;
+  };
+  auto all_loaded = [&] {
+    if (kInPlace) cluster_sync_all();
+  };
+  const int chunks = (n + step - 1) / step;
+  if (slice < 10) {  // 128 B a row; a warp instruction moves four rows, eight lanes a row
+    const int piece = lane & 7, sub = lane >> 3;
     const int64_t pitch = slice < 9 ? 1152 : 128;
     const uint8_t* from = (slice < 9 ? p.kv + slice * 128 : p.k_idx) + piece * 16;
     uint8_t* to = (slice < 9 ? p.to_kv + slice * 128 : p.to_k_idx) + piece * 16;
-    constexpr int kRows = kCompactThreads / 8;
-    for (int i0 = 0; i0 < n; i0 += kRows * kCompactUnroll) {
-      uint4 v[kCompactUnroll];
-      int64_t dst[kCompactUnroll];
+    uint4* mine = compact_smem + (warp * 32 + sub) * 8 + piece;  // + buffer, + 32 a group of rows
+    auto load = [&](int c) {
+      int slot;
+      const int row = c < chunks ? source(entry(c), slot) : -1;
 #pragma unroll
-      for (int u = 0; u < kCompactUnroll; ++u) {
-        int64_t src;
-        int slot;
-        rows_of(i0 + u * kRows + (tid >> 3), src, dst[u], slot);
-        if (src >= 0) v[u] = *reinterpret_cast<const uint4*>(from + src * pitch);
+      for (int j = 0; j < 8; ++j) {
+        const int r = __shfl_sync(0xffffffffu, row, j * 4 + sub);
+        if (r >= 0)
+          cp_async_16(smem_u32(mine + (c & 1) * kCompactRows * 8 + j * 32), from + r * pitch, 16u);
       }
-      __syncthreads();
+      cp_async_commit();
+      return row;
+    };
+    int row = load(0);
+    for (int c = 0; c < chunks; ++c) {
+      const int next = load(c + 1);
+      const int dst = row >= 0 ? destination(entry(c)) : -1;
+      cp_async_wait_group<1>();
+      all_loaded();
 #pragma unroll
-      for (int u = 0; u < kCompactUnroll; ++u)
-        if (dst[u] >= 0) *reinterpret_cast<uint4*>(to + dst[u] * pitch) = v[u];
+      for (int j = 0; j < 8; ++j) {
+        const int r = __shfl_sync(0xffffffffu, dst, j * 4 + sub);
+        if (r >= 0)
+          *reinterpret_cast<uint4*>(to + r * pitch) = mine[(c & 1) * kCompactRows * 8 + j * 32];
+      }
+      row = next;
     }
     return;
   }
-  for (int i0 = 0; i0 < n; i0 += kCompactThreads) {
-    int64_t src, dst;
-    int slot = 0;
-    float s = 0.f, m = 0.f;
-    rows_of(i0 + tid, src, dst, slot);
-    if (src >= 0) {
-      s = p.k_scale[src];
+  float s = 0.f, m = 0.f;
+  auto load = [&](int c) {
+    int slot;
+    const int row = c < chunks ? source(entry(c), slot) : -1;
+    if (row >= 0) {
+      s = p.k_scale[row];
       if (p.mass) m = p.mass[(int64_t)b * p.mass_ld + slot];
     }
-    __syncthreads();
+    return row;
+  };
+  int row = load(0);
+  for (int c = 0; c < chunks; ++c) {
+    const float s0 = s, m0 = m;
+    const int next = load(c + 1);
+    const int dst = row >= 0 ? destination(entry(c)) : -1;
+    all_loaded();
     if (dst >= 0) {
-      p.to_k_scale[dst] = s;
-      if (p.mass) p.to_mass[(int64_t)b * p.to_mass_ld + i0 + tid] = m;
+      p.to_k_scale[dst] = s0;
+      if (p.mass) p.to_mass[(int64_t)b * p.to_mass_ld + entry(c)] = m0;
     }
+    row = next;
   }
-  if (p.mass) {
-    __syncthreads();
-    for (int i = n + tid; i < min(len, p.to_max_ctx); i += kCompactThreads)
+  if (p.mass)
+    for (int i = n + rank * kCompactThreads + tid; i < min(len, p.to_max_ctx);
+         i += p.splits * kCompactThreads)
       p.to_mass[(int64_t)b * p.to_mass_ld + i] = 0.f;
-  }
 }
 
 }  // namespace dsa

@@ -917,6 +917,69 @@ dsa_status_t launch_rope(const void* x, const int32_t* positions, const double* 
   return cuda_status(cudaGetLastError());
 }
 
+// ---- eviction ----------------------------------------------------------------------
+// CTAs of a sequence: one for every 4096 slots, at most the portable cluster size.
+dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
+  static DeviceOnce once;
+  const cudaError_t attr_err = once_per_device(once, [] {
+    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kEvictMaxKeys * 4);
+  });
+  if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
+  p.splits = 1;
+  while (p.splits < 8 && (int64_t)p.splits * 4096 < p.max_ctx) p.splits *= 2;
+  const int64_t run = ((int64_t)p.max_ctx / p.splits + 32 + 31) & ~31ll;
+  p.held = run <= kEvictMaxKeys ? (int)run : 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((int64_t)batch * p.splits), 1, 1);
+  cfg.blockDim = dim3(kEvictThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)p.held * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, evict_select_kernel, p));
+}
+
+// ---- compact -----------------------------------------------------------------------
+// CTAs per slice: about three on every SM. In place they form a cluster (of at most
+// eight, the portable size), which moves its chunks in order.
+dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStream_t stream) {
+  static DeviceOnce once;
+  const cudaError_t attr_err = once_per_device(once, [] {
+    const cudaError_t e = cudaFuncSetAttribute(
+        cache_compact_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmemBytes);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(cache_compact_kernel<true>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       kCompactSmemBytes);
+  });
+  if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
+  const int64_t chunks = (p.keep + kCompactRows - 1) / kCompactRows;
+  const int64_t fill = (3 * num_sms() + (int64_t)batch * kCompactSlices - 1) /
+                       ((int64_t)batch * kCompactSlices);
+  p.splits = (int)std::min(chunks, fill);
+  if (in_place)
+    p.splits = p.splits >= 8 ? 8 : p.splits >= 4 ? 4 : p.splits >= 2 ? 2 : 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((int64_t)batch * p.splits), kCompactSlices, 1);
+  cfg.blockDim = dim3(kCompactThreads, 1, 1);
+  cfg.dynamicSmemBytes = kCompactSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = in_place ? p.splits : 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(in_place ? cudaLaunchKernelEx(&cfg, cache_compact_kernel<true>, p)
+                              : cudaLaunchKernelEx(&cfg, cache_compact_kernel<false>, p));
+}
+
 // ---- attention mass ----------------------------------------------------------------
 // Rows of a sequence up to which its rows' weights are added one row after another.
 constexpr int kMassFewRows = 8;
@@ -1527,9 +1590,8 @@ dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_d
   if ((reinterpret_cast<uintptr_t>(mass) & 3) || (reinterpret_cast<uintptr_t>(kept) & 3) ||
       (reinterpret_cast<uintptr_t>(new_lens) & 3))
     return DSA_ERR_INVALID_ARG;
-  EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent};
-  evict_select_kernel<<<(unsigned)g.batch, kEvictThreads, 0, (cudaStream_t)stream>>>(p);
-  return cuda_status(cudaGetLastError());
+  EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent, 1, 0};
+  return launch_evict(p, g.batch, (cudaStream_t)stream);
 }
 
 dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, float* mass,
@@ -1574,14 +1636,11 @@ dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, floa
   p.mass_ld = mass_ld;
   p.to_mass_ld = dst_mass_ld;
   p.keep = keep;
-  p.in_place = !dst;
   p.max_ctx = g.max_ctx, p.page_size = g.page_size, p.max_pages = g.max_pages;
   p.num_pages = g.num_pages;
   p.to_max_ctx = t.max_ctx, p.to_page_size = t.page_size, p.to_max_pages = t.max_pages;
   p.to_num_pages = t.num_pages;
-  cache_compact_kernel<<<dim3((unsigned)g.batch, kCompactSlices), kCompactThreads, 0,
-                         (cudaStream_t)stream>>>(p);
-  return cuda_status(cudaGetLastError());
+  return launch_compact(p, g.batch, !dst, (cudaStream_t)stream);
 }
 
 }  // extern "C"
