@@ -469,7 +469,7 @@ DSA_API dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const ds
  * mass (ties to the lower slot; -0 equals +0; NaN ranks below every number). A sequence
  * of at most `keep` tokens keeps them all.
  *  mass      fp32 [batch][mass_ld], mass_ld >= max_ctx, by slot
- *  kv        batch, max_ctx and seqlens are used
+ *  kv        batch, max_ctx (at most 2^22) and seqlens are used
  *  keep      >= 1 and >= sink + recent
  *  kept      int32 [batch][keep] out: the slots that stay, ascending, padded with -1
  *  new_lens  int32 [batch] out: min(seqlen, keep). */

@@ -923,17 +923,17 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t attr_err = once_per_device(once, [] {
     return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kEvictMaxKeys * 4);
+                                kEvictMaxDynamic);
   });
   if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
   p.splits = 1;
-  while (p.splits < 8 && (int64_t)p.splits * 4096 < p.max_ctx) p.splits *= 2;
-  const int64_t run = ((int64_t)p.max_ctx / p.splits + 32 + 31) & ~31ll;
-  p.held = run <= kEvictMaxKeys ? (int)run : 0;
+  while (p.splits < kEvictMaxSplits && (int64_t)p.splits * 4096 < p.max_ctx) p.splits *= 2;
+  p.run = (int)(((int64_t)p.max_ctx / p.splits + 32 + 31) & ~31ll);
+  p.hold = p.run <= kEvictMaxKeys;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)batch * p.splits), 1, 1);
   cfg.blockDim = dim3(kEvictThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)p.held * 4;
+  cfg.dynamicSmemBytes = (size_t)p.run / 4 + (p.hold ? (size_t)p.run * 4 : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1590,7 +1590,9 @@ dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_d
   if ((reinterpret_cast<uintptr_t>(mass) & 3) || (reinterpret_cast<uintptr_t>(kept) & 3) ||
       (reinterpret_cast<uintptr_t>(new_lens) & 3))
     return DSA_ERR_INVALID_ARG;
-  EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent, 1, 0};
+  if (g.max_ctx > kEvictMaxCtx) return DSA_ERR_UNSUPPORTED_SHAPE;
+  EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent,
+                1, 0, 0};
   return launch_evict(p, g.batch, (cudaStream_t)stream);
 }
 
