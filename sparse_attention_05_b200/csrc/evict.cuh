@@ -31,7 +31,7 @@ constexpr int kEvictMaxDynamic = kEvictMaxKeys * 4 + kEvictMaxKeys / 4;
 static_assert(kEvictMaxCtx / kEvictMaxSplits / 4 + 64 <= kEvictMaxDynamic, "bitmaps do not fit");
 
 struct EvictShared {
-  int hist[3][kEvictBins];
+  int hist[4][kEvictBins];      // of the three digits; [3]: the first digit's odd lanes
   int sums[3][kEvictWarps];     // of each group of bins, from the top down
   int scan[2][kEvictWarps];
   int counts[2];                // this CTA's slots above and at the border
@@ -91,8 +91,13 @@ __device__ __forceinline__ void evict_digit(EvictShared& sh, int pass, int left,
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
   {  // group `warp` from the top: bins 2047 - 128 warp downwards
-    const int4 c = *reinterpret_cast<const int4*>(
-        &sh.hist[pass][kEvictBins - kEvictGroup * (warp + 1) + 4 * lane]);
+    const int at = kEvictBins - kEvictGroup * (warp + 1) + 4 * lane;
+    int4 c = *reinterpret_cast<const int4*>(&sh.hist[pass][at]);
+    if (pass == 0) {
+      const int4 odd = *reinterpret_cast<const int4*>(&sh.hist[3][at]);
+      c.x += odd.x, c.y += odd.y, c.z += odd.z, c.w += odd.w;
+      *reinterpret_cast<int4*>(&sh.hist[0][at]) = c;
+    }
     const int s = __reduce_add_sync(0xffffffffu, c.x + c.y + c.z + c.w);
     if (lane == 0) sh.sums[pass][warp] = s;
   }
@@ -192,9 +197,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
   auto add = [&](int pass, int digit, uint32_t key, bool member) {
     const uint32_t zeros = __ballot_sync(0xffffffffu, member && key == kEvictZero);
     if (member && (key != kEvictZero || lane == __ffs(zeros) - 1))
-      atomicAdd(&sh.hist[pass][digit], key == kEvictZero ? __popc(zeros) : 1);
+      atomicAdd(&sh.hist[pass == 0 && (lane & 1) ? 3 : pass][digit],
+                key == kEvictZero ? __popc(zeros) : 1);
   };
-  for (int i = tid; i < 3 * kEvictBins; i += kEvictThreads) (&sh.hist[0][0])[i] = 0;
+  for (int i = tid; i < 4 * kEvictBins; i += kEvictThreads) (&sh.hist[0][0])[i] = 0;
   __syncthreads();
   for (int i0 = warp * 32; i0 < count; i0 += kEvictThreads * 8) {
     float m[8];  // eight loads of a thread in flight
