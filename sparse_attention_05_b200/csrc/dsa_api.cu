@@ -1031,8 +1031,13 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
     const cudaError_t e = cudaMemsetAsync(workspace, 0, (size_t)g.batch * g.max_ctx * 8, stream);
     if (e != cudaSuccess) return DSA_ERR_CUDA;
   }
-  attn_mass_kernel<<<(unsigned)((int64_t)g.batch * g.row_count), kMassThreads, kMassSmemBytes,
-                     stream>>>(p);
+  // equal runs of tiles balance few rows; with sixteen rows and more a CTA, whole rows in
+  // turn are as even and spread the short ones (and load each Q once)
+  const int64_t rows = (int64_t)g.batch * g.row_count, tiles = (k + kMassTile - 1) / kMassTile;
+  const int sms = num_sms();
+  p.whole_rows = rows >= 16ll * sms;
+  const unsigned grid = (unsigned)std::min<int64_t>(sms, p.whole_rows ? rows : rows * tiles);
+  attn_mass_kernel<<<grid, kMassThreads, kMassSmemBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (few)
     mass_add_rows_kernel<<<(unsigned)g.batch, 512, 0, stream>>>(p);
