@@ -6,23 +6,32 @@
 // The head mean is the main attention's distribution of the report's §2.1.
 //
 // Per listed entry 1152 B gathered and 147456 flops: 128 flops a byte, below the ~253
-// at which this part's BF16 rate and HBM rate meet, so rows gathered from HBM are bound
-// by the gather; rows that L2 holds by the L2 -> SM gather and the tensor core alike.
-// One persistent CTA per SM walks (row, 128-entry tile) items: with few rows an equal run
-// of all rows' tiles each (a row may be shared by several CTAs), with many every
-// gridDim-th row whole, which spreads the short rows evenly.
-// The row's Q (128 heads x 576) stays in shared memory as nine 128-B-swizzled chunks of 64
-// dims, the listed latent rows stream through a ring of 64-dim chunks, and
-// D[entry][head] = K_tile (128 x 576) . Q^T lands in one of two TMEM accumulators, entries
-// on the lanes, so that the sum over heads stays inside a thread. The next row's Q chunk c
-// travels with its first tile's chunk c: the ring stage it takes is free only once the
-// last row's products with chunk c are done (the ring is shorter than a tile).
-// Tiles without a single valid entry are passed over by every role alike.
+// at which this part's BF16 rate and HBM rate meet, so the gather bounds the kernel:
+// rows in HBM come at 5.2-5.9 TB/s with 112-200 KB of loads in flight per SM and 4.3 with
+// 80 KB, rows in L2 at up to 10.5 TB/s (measured, loads alone). Hence Q does not take
+// shared memory: the row's Q (128 heads x 576) is the A operand in tensor memory (288
+// columns), and shared memory is a ring of seven 28-KB stages for the listed latent rows,
+// 64 dims of up to 224 rows each. D[head][entry] = Q . K_tile^T takes the other 224
+// columns: N = 224 costs the tensor core about what N = 128 does (the operand in tensor
+// memory is read at one rate for both), so a wide tile is nearly free.
 //
-// Warp roles (288 threads): 0-3 epilogue (thread = entry), 4 TMEM and MMA issue, 5-8
-// producers (a warp's cp.async covers four whole 128-B lines, eight lanes a line; one
-// line a lane would take eight times the tag lookups). Entries are read two tiles ahead
-// and their pages one tile ahead.
+// One persistent CTA per SM walks (row, tile) items: with few rows an equal run of all
+// rows' tiles each (a row may be shared by several CTAs), with many every gridDim-th row
+// whole, which spreads the short rows evenly. A row's Q travels through the ring as nine
+// stages before its first tile. Tiles without a valid entry are passed over by every role.
+//
+// Warp roles (512 threads):
+//   warps 0-11  epilogue: warp w has heads 32 (w % 4) .. + 31 on its lanes and the columns
+//               of third w / 4 (80, 80 and 64). It empties the accumulator into registers
+//               (there is one: the tensor core waits for no more than that), takes the
+//               exponentials, and sums each column over its lanes by halving exchanges;
+//               the four partial sums of a column meet in shared memory
+//   warp 12     TMEM, and the issue of the copies of Q into it and of the products
+//   warps 13-15 producers: a warp's cp.async covers four whole 128-B lines, eight lanes a
+//               line (one line a lane would take eight times the tag lookups). Entries are
+//               read two tiles ahead and their pages one tile ahead. Where the list has
+//               no entry the cache's first row is copied and its column dropped (a copy
+//               with a zero-fill operand takes 1.6 times as long to issue).
 //
 // The sums over the rows are the same for every order of execution:
 //   few rows a sequence: p goes to the workspace, and one CTA a sequence adds its rows
@@ -41,14 +50,17 @@ namespace dsa {
 constexpr int kMassHeads = 128;
 constexpr int kMassDqk = 576;
 constexpr int kMassChunks = kMassDqk / 64;
-constexpr int kMassTile = 128;
-constexpr int kMassStages = 5;
-constexpr int kMassThreads = 288;
-constexpr int kMassChunkBytes = 128 * 128;
-constexpr int kMassSmemBytes = 1024 + (kMassChunks + kMassStages) * kMassChunkBytes +
-                               2 * kMassHeads * 4 + 24 * 8 + 16;
-static_assert(kMassStages <= kMassChunks, "a Q chunk must be free when its ring stage is");
+constexpr int kMassMaxTile = 224;                  // entries of a tile (MMA N), at most
+constexpr int kMassThird = 80;                     // columns of an epilogue warp, at most
+constexpr int kMassStages = 7;
+constexpr int kMassStageBytes = kMassMaxTile * 128;
+constexpr int kMassEpilogue = 384, kMassProducers = 96;
+constexpr int kMassThreads = kMassEpilogue + 32 + kMassProducers;
+constexpr int kMassQCols = kMassDqk / 2;           // tensor memory columns of Q
+constexpr int kMassSmemBytes = 1024 + kMassStages * kMassStageBytes +
+                               2 * 4 * kMassMaxTile * 4 /*partial sums*/ + 24 * 8 + 16;
 static_assert(kMassSmemBytes <= 232448, "attention mass shared memory exceeds the per-CTA limit");
+static_assert(kMassQCols + kMassMaxTile <= 512, "tensor memory");
 constexpr float kMassUnit = 1099511627776.0f;             // 2^40 units of fixed point
 constexpr float kMassMaxP = 64.0f;                        // a larger p is not a weight
 constexpr unsigned long long kMassNan = 1ull << 63;       // set, never added
@@ -68,229 +80,309 @@ struct MassParams {
   int32_t k, batch, max_ctx, q_per_seq, num_q;
   int32_t row_begin, row_count;
   int32_t paged, page_size, max_pages, num_pages;
+  int32_t tile;                // entries of a tile: a multiple of 16, at most 224
+  int32_t ntiles;              // of a row
   int32_t whole_rows;          // CTAs take whole rows instead of runs of tiles
   float scale_log2;
   uint64_t timeout_ns;
 };
 
-// The (row, tile) items of one CTA, in order.
+// The (row, tile) items of one CTA, in order. (Rows, and one CTA's items, are below 2^31.)
 struct MassItems {
-  int64_t row, end;    // window row, and the end (rows, or the CTA's last item)
+  int row;             // window row
+  int left;            // items after this one (runs of tiles)
   int tile, b, pos;
-  int64_t t;           // global query row, -1: the sequence does not have it
+  int t;               // global query row, -1: the sequence does not have it
   bool live;           // there is an item
 
   __device__ __forceinline__ void start(const MassParams& p) {
-    const int ntiles = (p.k + kMassTile - 1) / kMassTile;
     const int64_t rows = (int64_t)p.batch * p.row_count;
     tile = 0;
     if (p.whole_rows) {
       row = blockIdx.x;
-      end = rows;
-      live = row < end;
+      left = 0;
+      live = row < rows;
     } else {
+      const int ntiles = p.ntiles;
       const int64_t first = rows * ntiles * blockIdx.x / gridDim.x;
-      end = rows * ntiles * (blockIdx.x + 1) / gridDim.x;
-      live = first < end;
-      row = first / ntiles;
-      tile = (int)(first - row * ntiles);
+      left = (int)(rows * ntiles * (blockIdx.x + 1) / gridDim.x - first) - 1;
+      live = left >= 0;
+      row = (int)(first / ntiles);
+      tile = (int)(first - (int64_t)row * ntiles);
     }
     if (live) find(p);
   }
   __device__ __forceinline__ void find(const MassParams& p) {
-    b = (int)(row / p.row_count);
-    const int qi = p.row_begin + (int)(row - (int64_t)b * p.row_count);
+    b = row / p.row_count;
+    const int qi = p.row_begin + row - b * p.row_count;
     const SeqRows R = seq_rows(p.q_start, p.seqlens, b, p.q_per_seq, p.num_q, p.max_ctx);
-    t = R.ok && qi < R.q_len ? R.t0 + qi : -1;
+    t = R.ok && qi < R.q_len ? (int)R.t0 + qi : -1;
     pos = R.seqlen - R.q_len + qi;
     if (!R.ok) report_error(kErrBounds);
   }
   __device__ __forceinline__ void next(const MassParams& p) {
-    const int ntiles = (p.k + kMassTile - 1) / kMassTile;
-    if (t >= 0 && ++tile < ntiles) {
-      live = p.whole_rows || row * ntiles + tile < end;
+    const int ntiles = p.ntiles;
+    if (t >= 0 && tile + 1 < ntiles) {
+      ++tile;
+      live = p.whole_rows || --left >= 0;
       return;
     }
+    if (p.whole_rows) {
+      live = (int64_t)row + gridDim.x < (int64_t)p.batch * p.row_count;
+      row += gridDim.x;
+    } else {
+      left -= ntiles - tile;  // the rest of a row that the sequence does not have
+      live = left >= 0;
+      ++row;
+    }
     tile = 0;
-    row += p.whole_rows ? gridDim.x : 1;
-    live = p.whole_rows ? row < end : row * ntiles < end;
     if (live) find(p);
   }
-  // Entry e of the tile: its slot, or -1.
-  __device__ __forceinline__ int entry(const MassParams& p, int e) const {
-    const int i = tile * kMassTile + e;
-    if (!live || t < 0 || i >= p.k) return -1;
-    const int sel = __ldg(p.idx + t * p.k + i);
-    return sel <= pos ? max(sel, -1) : -1;
+  // Entry e of the tile as it is listed, -1 past the list. Nothing here waits for the load.
+  __device__ __forceinline__ int listed(const MassParams& p, int e) const {
+    const int i = tile * p.tile + e;
+    return live && t >= 0 && e < p.tile && i < p.k ? __ldg(p.idx + (int64_t)t * p.k + i) : -1;
+  }
+  __device__ __forceinline__ bool valid(int sel) const { return sel >= 0 && sel <= pos; }
+  // Columns of the tile's MMA: its entries, to a multiple of 16.
+  __device__ __forceinline__ int columns(const MassParams& p) const {
+    return (min(p.tile, p.k - tile * p.tile) + 15) & ~15;
   }
 };
 
-// Whether any of a tile's 128 entries is one, told from four per lane.
-__device__ __forceinline__ bool mass_tile_used(const int (&sel)[4]) {
-  return __any_sync(0xffffffffu, (sel[0] & sel[1] & sel[2] & sel[3]) >= 0);
+// Whether a tile has an entry at all. Only a row that sees fewer keys than the list is long
+// can have a tile without one (or one that lists keys twice, which it may compute in vain).
+__device__ __forceinline__ bool mass_used(const MassParams& p, const MassItems& m, int lane) {
+  if (!m.live || m.t < 0) return false;
+  if (m.pos + 1 >= p.k) return true;
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < kMassMaxTile / 32; ++i) any |= m.valid(m.listed(p, i * 32 + lane));
+  return __any_sync(0xffffffffu, any);
+}
+
+// 128 rows of 32 bytes from shared memory (descriptor as an MMA operand's) to the 128 lanes
+// of eight tensor memory columns, ordered before the products issued after it.
+__device__ __forceinline__ void tmem_copy_128x32(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Place in the ring: stage and the parity of its round.
+struct MassRing {
+  int stage = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kMassStages) stage = 0, round ^= 1;
+  }
+};
+
+// Weights of N columns of this lane's head, and their sums over the warp's lanes: lane l
+// gets column l's (N = 16: columns 0-15 twice). Every column is summed in the same order.
+template <int N>
+__device__ __forceinline__ float mass_columns(uint32_t (&z)[N], float scale_log2, float lse2,
+                                              int lane) {
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    v[i] = ex2_approx(fmaf(__uint_as_float(z[i]), scale_log2, -lse2));
+  if (N == 16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+  }
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  return v[0];
 }
 
 __global__ void __launch_bounds__(kMassThreads, 1)
     attn_mass_kernel(const __grid_constant__ MassParams p) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* sQ = smem;
-  uint8_t* sK = sQ + kMassChunks * kMassChunkBytes;
-  float* sLse2 = reinterpret_cast<float*>(sK + kMassStages * kMassChunkBytes);  // [2][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sLse2 + 2 * kMassHeads);
-  uint64_t* kfull = bars;                    // [stages] the chunk (and its Q chunk) landed
-  uint64_t* kempty = kfull + kMassStages;    // [stages] its products are done
-  uint64_t* tfull = kempty + kMassStages;    // [2] accumulator ready
-  uint64_t* tempty = tfull + 2;              // [2] read
-  uint64_t* mdone = tempty + 2;
+  float* sPart = reinterpret_cast<float*>(ring + kMassStages * kMassStageBytes);  // [2][4][224]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sPart + 2 * 4 * kMassMaxTile);
+  uint64_t* kfull = bars;                    // [stages] the stage's copies are complete
+  uint64_t* kempty = kfull + kMassStages;    // [stages] it was read
+  uint64_t* tfull = kempty + kMassStages;    // the accumulator is ready
+  uint64_t* tempty = tfull + 1;              // it is in registers
+  uint64_t* mdone = tempty + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mdone + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kMassStages; ++i) {
-      mbar_init(smem_u32(&kfull[i]), 128);
+      mbar_init(smem_u32(&kfull[i]), kMassProducers);
       mbar_init(smem_u32(&kempty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&tfull[i]), 1);
-      mbar_init(smem_u32(&tempty[i]), 128);
-    }
+    mbar_init(smem_u32(tfull), 1);
+    mbar_init(smem_u32(tempty), kMassEpilogue / 32);
     mbar_init(smem_u32(mdone), 1);
     *abort_flag = 0;
     fence_mbarrier_init_cluster();
   }
-  if (warp == 4) {
-    tmem_alloc(smem_u32(tmem_holder), 256);
+  if (warp == 12) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
+  const uint32_t tmem_q = *tmem_holder, tmem_d = tmem_q + kMassQCols;
   const uint64_t TO = p.timeout_ns;
   int drain_dummy = 0;
   volatile int* no_abort = &drain_dummy;
 
-  if (warp >= 5) {
+  if (warp >= 13) {
     // ------------------------------------------------------------ producers
-    const int pw = warp - 5, piece = lane & 7, sub = lane >> 3;
-    auto load_entries = [&](const MassItems& m, int (&sel)[4]) {
+    const int pw = warp - 13, piece = lane & 7, sub = lane >> 3;
+    // rows of this warp: per from pw * per on, a multiple of four
+    const int per = (p.tile / 4 + 2) / 3 * 4;
+    constexpr int kGroups = (kMassMaxTile / 4 + 2) / 3;  // of four rows
+    // this lane's entries pw * per + lane, + 32 and + 64 of the tile
+    auto own_entries = [&](const MassItems& m, int (&own)[3]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sel[i] = m.entry(p, i * 32 + lane);
-    };
-    // the page of this lane's own entry (entry pw * 32 + lane of the tile)
-    auto own = [&](const int (&sel)[4]) {
-      return pw == 0 ? sel[0] : pw == 1 ? sel[1] : pw == 2 ? sel[2] : sel[3];
+      for (int i = 0; i < 3; ++i)
+        own[i] = lane + 32 * i < per ? m.listed(p, pw * per + lane + 32 * i) : -1;
     };
     auto load_page = [&](const MassItems& m, int s) {
-      return p.paged && s >= 0
+      return p.paged && m.valid(s)
                  ? __ldg(p.block_table + (int64_t)m.b * p.max_pages + s / p.page_size) : 0;
     };
+    auto cache_row_of = [&](const MassItems& m, int s, int page) {
+      if (!m.valid(s)) return 0;
+      if (!p.paged) return m.b * p.max_ctx + s;
+      if (page >= 0 && page < p.num_pages) return page * p.page_size + s % p.page_size;
+      report_error(kErrBounds);
+      return 0;
+    };
+    MassRing at;
+    bool ok = true;
+    auto acquire = [&] {
+      const uint32_t bar = smem_u32(&kempty[at.stage]);
+      if (!__all_sync(0xffffffffu, mbar_test_wait(bar, at.round ^ 1)))
+        ok = warp_wait(bar, at.round ^ 1, TO, abort_flag);
+      return ok;
+    };
+    // where this lane's 16 bytes of a four-row group lie in a stage: rows alternate between
+    // two phases of the swizzle
+    const uint32_t even = sw128_offset(pw * per + sub, piece);
+    const uint32_t odd = sw128_offset(pw * per + 4 + sub, piece) - 512;
     MassItems cur, ahead, far;  // this tile's, one and two tiles ahead
-    int s0[4], s1[4], s2[4];
+    int own0[3], own1[3], own2[3], page0[3], page1[3];
     cur.start(p);
-    load_entries(cur, s0);
+    own_entries(cur, own0);
     ahead = cur;
     if (ahead.live) ahead.next(p);
-    load_entries(ahead, s1);
+    own_entries(ahead, own1);
     far = ahead;
-    int page0 = load_page(cur, own(s0));
-    int64_t q_row = -1;  // the query row whose Q is in shared memory
-    uint32_t it = 0;
-    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) page0[i] = load_page(cur, own0[i]);
+    int q_row = -1;  // the query row whose Q went through the ring last
     while (cur.live && ok) {
-      const int page1 = load_page(ahead, own(s1));
+#pragma unroll
+      for (int i = 0; i < 3; ++i) page1[i] = load_page(ahead, own1[i]);
       if (far.live) far.next(p);
-      load_entries(far, s2);
-      if (mass_tile_used(s0)) {
-        const int sel = own(s0);
-        int row = -1;
-        if (sel >= 0) {
-          if (!p.paged)
-            row = cur.b * p.max_ctx + sel;
-          else if (page0 >= 0 && page0 < p.num_pages)
-            row = page0 * p.page_size + sel % p.page_size;
-          else
-            report_error(kErrBounds);
-        }
-        int rows[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rows[i] = __shfl_sync(0xffffffffu, row, i * 4 + sub);
-        const bool new_q = cur.t != q_row;
-        q_row = cur.t;
-        const uint8_t* q = reinterpret_cast<const uint8_t*>(p.q + cur.t * kMassHeads * kMassDqk);
+      own_entries(far, own2);
+      if (mass_used(p, cur, lane)) {
+        if (cur.t != q_row) {
+          q_row = cur.t;
+          const uint8_t* q =
+              reinterpret_cast<const uint8_t*>(p.q + (int64_t)q_row * kMassHeads * kMassDqk) + piece * 16;
 #pragma unroll 1
-        for (int c = 0; c < kMassChunks; ++c, ++it) {
-          const int st = it % kMassStages;
-          if (!warp_wait(smem_u32(&kempty[st]), ((it / kMassStages) & 1) ^ 1, TO, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t dst = smem_u32(sK + st * kMassChunkBytes);
-          const int off = c * 128 + piece * 16;
+          for (int c = 0; c < kMassChunks && ok; ++c) {
+            if (!acquire()) break;
+            const uint32_t dst = smem_u32(ring + at.stage * kMassStageBytes);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            cp_async_16(dst + sw128_offset(pw * 32 + i * 4 + sub, piece),
-                        p.kv + (int64_t)max(rows[i], 0) * (kMassDqk * 2) + off,
-                        rows[i] >= 0 ? 16u : 0u);
-          if (new_q) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int h = pw * 32 + i * 4 + sub;
-              cp_async_16(smem_u32(sQ + c * kMassChunkBytes) + sw128_offset(h, piece),
-                          q + h * (kMassDqk * 2) + off, 16u);
+            for (int i = 0; i < 11; ++i) {
+              const int h = (pw * 11 + i) * 4 + sub;
+              if (h < kMassHeads)
+                cp_async_16(dst + sw128_offset(h, piece), q + h * (kMassDqk * 2) + c * 128, 16u);
             }
+            cp_async_mbar_arrive(smem_u32(&kfull[at.stage]));
+            at.next();
           }
-          cp_async_mbar_arrive(smem_u32(&kfull[st]));
+        }
+        int mine[3];
+        const uint8_t* rows[kGroups];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) mine[i] = cache_row_of(cur, own0[i], page0[i]);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i)
+          rows[i] = p.kv + piece * 16 + (int64_t)(kMassDqk * 2) *
+                    __shfl_sync(0xffffffffu, mine[i / 8], (i * 4 + sub) & 31);
+        const int groups = min(per, max(0, cur.columns(p) - pw * per)) / 4;
+#pragma unroll
+        for (int c = 0; c < kMassChunks; ++c) {
+          if (!acquire()) break;
+          const uint32_t dst = smem_u32(ring + at.stage * kMassStageBytes);
+          const uint32_t dst_even = dst + even, dst_odd = dst + odd;
+#pragma unroll
+          for (int i = 0; i < kGroups; ++i)
+            if (i < groups)
+              cp_async_16((i & 1 ? dst_odd : dst_even) + i * 512, rows[i] + c * 128, 16u);
+          cp_async_mbar_arrive(smem_u32(&kfull[at.stage]));
+          at.next();
         }
       }
       cur = ahead;
       ahead = far;
-      page0 = page1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s0[i] = s1[i], s1[i] = s2[i];
+      for (int i = 0; i < 3; ++i) own0[i] = own1[i], own1[i] = own2[i], page0[i] = page1[i];
     }
     cp_async_wait_all();
-  } else if (warp == 4) {
+  } else if (warp == 12) {
     // ------------------------------------------------------------ MMA issuer
-    const uint32_t idesc = instr_desc(1 /*bf16*/, 0, 0, 128, 128);
-    uint32_t it = 0, tiles = 0;
+    MassRing at;
+    uint32_t tiles = 0;
     bool ok = true;
+    int q_row = -1;
     MassItems m;
     m.start(p);
-    int sel[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sel[i] = m.entry(p, i * 32 + lane);
     while (m.live && ok) {
-      const bool used = mass_tile_used(sel);
+      const MassItems now = m;
+      const bool used = mass_used(p, m, lane);
       m.next(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sel[i] = m.entry(p, i * 32 + lane);  // the next tile's
       if (!used) continue;
-      const int ab = tiles & 1;
+      const bool new_q = now.t != q_row;
+      q_row = now.t;
+      const uint32_t idesc = instr_desc(1 /*bf16*/, 0, 0, 128, now.columns(p));
       if (lane == 0) {
-        ok = mbar_wait(smem_u32(&tempty[ab]), ((tiles >> 1) & 1) ^ 1, TO, abort_flag);
+        // the accumulator was read, so all products before are done, and Q may be replaced
+        ok = mbar_wait(smem_u32(tempty), (tiles & 1) ^ 1, TO, abort_flag);
         tc_fence_after();
-        const uint32_t d = tmem_base + ab * 128;
-        for (int c = 0; c < kMassChunks && ok; ++c, ++it) {
-          const int st = it % kMassStages;
-          ok = mbar_wait(smem_u32(&kfull[st]), (it / kMassStages) & 1, TO, abort_flag);
+        const int stages = (new_q ? 2 : 1) * kMassChunks;
+        MassRing st = at;
+        for (int i = 0; i < stages && ok; ++i, st.next()) {
+          ok = mbar_wait(smem_u32(&kfull[st.stage]), st.round, TO, abort_flag);
           if (!ok) break;
           tc_fence_after();
           fence_proxy_async_smem();  // cp.async (generic proxy) writes -> tensor-core reads
-          const uint32_t ka = smem_u32(sK + st * kMassChunkBytes);
-          const uint32_t qa = smem_u32(sQ + c * kMassChunkBytes);
+          const uint32_t src = smem_u32(ring + st.stage * kMassStageBytes);
+          const int c = stages - i <= kMassChunks ? i - (stages - kMassChunks) : -1;
+          if (c < 0) {  // a chunk of Q; the products that follow see it
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ss(d, smem_desc_sw128(ka + kk * 32, 16, 1024),
-                        smem_desc_sw128(qa + kk * 32, 16, 1024), idesc, (c > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(smem_u32(&kempty[st]));
+            for (int kk = 0; kk < 4; ++kk)
+              tmem_copy_128x32(tmem_q + i * 32 + kk * 8, smem_desc_sw128(src + kk * 32, 16, 1024));
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(tmem_d, tmem_q + c * 32 + kk * 8, smem_desc_sw128(src + kk * 32, 16, 1024),
+                          idesc, (c > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(smem_u32(&kempty[st.stage]));
         }
-        if (ok) mma_commit(smem_u32(&tfull[ab]));
+        if (ok) mma_commit(smem_u32(tfull));
       }
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      for (int i = 0; i < (new_q ? 2 : 1) * kMassChunks; ++i) at.next();
       ++tiles;
     }
     if (lane == 0) {
@@ -300,49 +392,59 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const int quad = warp & 3, third = warp >> 2;
+    const int head = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     uint32_t tiles = 0;
-    int lse_buf = 0;
-    int64_t lse_row = -1;
     MassItems m;
     m.start(p);
-    int sel[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sel[i] = m.entry(p, i * 32 + lane);
+    auto load_lse = [&](const MassItems& i) {
+      return i.live && i.t >= 0 ? __ldg(p.lse + (int64_t)i.t * kMassHeads + head) : 0.f;
+    };
+    int sel = m.listed(p, tid);
+    float next_lse = load_lse(m);
     while (m.live) {
-      const bool used = mass_tile_used(sel);
-      const int slot = warp == 0 ? sel[0] : warp == 1 ? sel[1] : warp == 2 ? sel[2] : sel[3];
       const MassItems now = m;
+      const float lse2 = next_lse * 1.4426950408889634f;
+      const bool now_used = mass_used(p, m, lane);
+      const int slot = m.valid(sel) ? sel : -1;
       m.next(p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sel[i] = m.entry(p, i * 32 + lane);
+      sel = m.listed(p, tid);
+      if (m.t != now.t) next_lse = load_lse(m);
       float w = 0.f;
-      if (used) {
-        if (now.t != lse_row) {  // double-buffered: the four warps are at most a barrier apart
-          lse_row = now.t;
-          lse_buf ^= 1;
-          sLse2[lse_buf * kMassHeads + tid] =
-              __ldg(p.lse + now.t * kMassHeads + tid) * 1.4426950408889634f;
-        }
-        const int ab = tiles & 1;
-        const bool got = warp_wait(smem_u32(&tfull[ab]), (tiles >> 1) & 1, TO, abort_flag);
-        if (!named_barrier_and(1, 128, got)) break;
+      if (now_used) {
+        // Warp 0 alone polls; the others sleep at the named barrier
+        const bool got = warp != 0 || warp_wait(smem_u32(tfull), tiles & 1, TO, abort_flag);
+        if (!named_barrier_and(1, kMassEpilogue, got)) break;
         tc_fence_after();
-        const float* lse2 = sLse2 + lse_buf * kMassHeads;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float z[32];
-          tmem_ld32(tmem_base + ab * 128 + c * 32 + lane_off, z);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) w += ex2_approx(z[i] * p.scale_log2 - lse2[c * 32 + i]);
-        }
+        uint32_t za[32], zb[32], zc[16];
+        const uint32_t col = tmem_d + lane_off + third * kMassThird;
+        tmem_ld32u(col, za);
+        tmem_ld32u(col + 32, zb);
+        if (third < 2) tmem_ld16u(col + 64, zc);
+        tmem_wait_ld_fence(za);
+        tmem_wait_ld_fence(zb);
+        tmem_wait_ld_fence16(zc);
         tc_fence_before();
-        mbar_arrive(smem_u32(&tempty[ab]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(tempty));
+        const int n = now.columns(p) - third * kMassThird;
+        float* part = sPart + ((tiles & 1) * 4 + quad) * kMassMaxTile + third * kMassThird;
+        if (n > 0) part[lane] = mass_columns(za, p.scale_log2, lse2, lane);
+        if (n > 32) part[32 + lane] = mass_columns(zb, p.scale_log2, lse2, lane);
+        if (n > 64 && third < 2) {
+          const float v = mass_columns(zc, p.scale_log2, lse2, lane);
+          if (lane < 16) part[64 + lane] = v;
+        }
+        named_barrier_sync(2, kMassEpilogue);
+        if (tid < kMassMaxTile) {
+          const float* all = sPart + (tiles & 1) * 4 * kMassMaxTile + tid;
+          w = (all[0] + all[kMassMaxTile]) + (all[2 * kMassMaxTile] + all[3 * kMassMaxTile]);
+        }
         ++tiles;
       }
       w *= 1.0f / kMassHeads;
-      const int e = now.tile * kMassTile + tid;
+      const int e = now.tile * p.tile + tid;
       if (p.sums) {
         if (slot >= 0) {
           unsigned long long* s = p.sums + (int64_t)now.b * p.max_ctx + slot;
@@ -351,8 +453,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           else
             atomicOr(s, kMassNan);
         }
-      } else if (now.t >= 0 && e < p.k) {
-        p.p_out[now.row * p.k + e] =
+      } else if (now.t >= 0 && tid < p.tile && e < p.k) {
+        p.p_out[(int64_t)now.row * p.k + e] =
             slot < 0 ? 0.f : w <= kMassMaxP ? w : __int_as_float(0x7fffffff);
       }
     }
@@ -361,9 +463,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, 256);
+    tmem_dealloc(tmem_q, 512);
   }
 }
 

@@ -1031,12 +1031,21 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
     const cudaError_t e = cudaMemsetAsync(workspace, 0, (size_t)g.batch * g.max_ctx * 8, stream);
     if (e != cudaSuccess) return DSA_ERR_CUDA;
   }
+  // As few tiles a row as the widest one gives, all about as wide; narrower ones where the
+  // tiles would not give every SM one, down to 64 entries, below which loading Q (128 rows
+  // of the same length) dominates.
+  const int64_t rows = (int64_t)g.batch * g.row_count;
+  const int sms = num_sms();
+  const int per_row = (int)std::max<int64_t>(
+      (k + kMassMaxTile - 1) / kMassMaxTile,
+      std::min<int64_t>((sms + rows - 1) / rows, (k + 63) / 64));
+  p.tile = (k + per_row * 16 - 1) / (per_row * 16) * 16;
+  p.ntiles = (k + p.tile - 1) / p.tile;
+  const int64_t tiles = rows * p.ntiles;
   // equal runs of tiles balance few rows; with sixteen rows and more a CTA, whole rows in
   // turn are as even and spread the short ones (and load each Q once)
-  const int64_t rows = (int64_t)g.batch * g.row_count, tiles = (k + kMassTile - 1) / kMassTile;
-  const int sms = num_sms();
   p.whole_rows = rows >= 16ll * sms;
-  const unsigned grid = (unsigned)std::min<int64_t>(sms, p.whole_rows ? rows : rows * tiles);
+  const unsigned grid = (unsigned)std::min<int64_t>(sms, p.whole_rows ? rows : tiles);
   attn_mass_kernel<<<grid, kMassThreads, kMassSmemBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (few)
