@@ -21,11 +21,13 @@
 // stages before its first tile. Tiles without a valid entry are passed over by every role.
 //
 // Warp roles (512 threads):
-//   warps 0-11  epilogue: warp w has heads 32 (w % 4) .. + 31 on its lanes and the columns
-//               of third w / 4 (80, 80 and 64). It empties the accumulator into registers
-//               (there is one: the tensor core waits for no more than that), takes the
-//               exponentials, and sums each column over its lanes by halving exchanges;
-//               the four partial sums of a column meet in shared memory
+//   warps 0-11  epilogue: warp w has heads 32 (w % 4) .. + 31 and the columns of third
+//               w / 4 (80, 80 and 64). It empties the accumulator into registers (there
+//               is one: the tensor core waits for no more than that), four heads of a
+//               column in a thread, takes the exponentials and sums a column in the thread
+//               and over the eight lanes that share it (with one head a lane the sums took
+//               31 exchanges for 32 columns, not 7, and 512 rows 215 us, not 199); the
+//               four partial sums of a column meet in shared memory
 //   warp 12     TMEM, and the issue of the copies of Q into it and of the products
 //   warps 13-15 producers: a warp's cp.async covers four whole 128-B lines, eight lanes a
 //               line (one line a lane would take eight times the tag lookups). Entries are
@@ -176,30 +178,78 @@ struct MassRing {
   }
 };
 
-// Weights of N columns of this lane's head, and their sums over the warp's lanes: lane l
-// gets column l's (N = 16: columns 0-15 twice). Every column is summed in the same order.
-template <int N>
-__device__ __forceinline__ float mass_columns(uint32_t (&z)[N], float scale_log2, float lse2,
-                                              int lane) {
-  float v[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    v[i] = ex2_approx(fmaf(__uint_as_float(z[i]), scale_log2, -lse2));
-  if (N == 16) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
-  }
-#pragma unroll
-  for (int o = N / 2; o > 0; o >>= 1) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
-  }
-  return v[0];
+// 16 lanes x 32 (or 16) columns of tensor memory: register 4 j + 2 r + c of a thread holds
+// lane l / 4 + 8 r, column 8 j + 2 (l % 4) + c (l: the thread's lane).
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for this thread's tensor memory loads; ties the registers to the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld_tie(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// A block of 8 G columns of a warp's 32 heads: this thread's logits of heads l / 4 and + 8
+// (lo), + 16 and + 24 (hi).
+template <int G>
+struct MassBlock {
+  uint32_t lo[4 * G], hi[4 * G];
+  __device__ __forceinline__ void load(uint32_t taddr) {
+    tmem_ld_16x256b(taddr, lo);
+    tmem_ld_16x256b(taddr + (16u << 16), hi);
+  }
+  __device__ __forceinline__ void wait() {
+    tmem_wait_ld_tie(lo);
+    tmem_wait_ld_tie(hi);
+  }
+  // The weights, summed over the warp's heads: four in the thread, then halving exchanges
+  // over the eight lanes that share its columns. Every column is summed in the same order.
+  // Lane l gets column 16 b4 + 8 b3 + b2 + 2 (l % 4) by its bits (G = 2: without b4's).
+  __device__ __forceinline__ float sum(float scale_log2, const float (&lse2)[4], int lane) const {
+    auto weight = [&](uint32_t z, int r) {
+      return ex2_approx(fmaf(__uint_as_float(z), scale_log2, -lse2[r]));
+    };
+    float v[2 * G];
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        v[2 * j + c] = (weight(lo[4 * j + c], 0) + weight(lo[4 * j + 2 + c], 1)) +
+                       (weight(hi[4 * j + c], 2) + weight(hi[4 * j + 2 + c], 3));
+    }
+    if (G == 2) {
+#pragma unroll
+      for (int i = 0; i < 2 * G; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    }
+#pragma unroll
+    for (int n = G, o = G == 2 ? 8 : 16; n > 0; n >>= 1, o >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+    return v[0];
+  }
+};
 
 __global__ void __launch_bounds__(kMassThreads, 1)
     attn_mass_kernel(const __grid_constant__ MassParams p) {
@@ -393,48 +443,56 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3, third = warp >> 2;
-    const int head = quad * 32 + lane;
+    const int head = quad * 32 + (lane >> 2);  // and + 8, + 16, + 24
+    const int column = (lane & 16) + (lane & 8) + ((lane >> 2) & 1) + 2 * (lane & 3);
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     uint32_t tiles = 0;
     MassItems m;
     m.start(p);
+    float next_lse[4] = {0.f, 0.f, 0.f, 0.f};
     auto load_lse = [&](const MassItems& i) {
-      return i.live && i.t >= 0 ? __ldg(p.lse + (int64_t)i.t * kMassHeads + head) : 0.f;
+      if (!i.live || i.t < 0) return;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        next_lse[r] = __ldg(p.lse + (int64_t)i.t * kMassHeads + head + 8 * r);
     };
     int sel = m.listed(p, tid);
-    float next_lse = load_lse(m);
+    load_lse(m);
     while (m.live) {
       const MassItems now = m;
-      const float lse2 = next_lse * 1.4426950408889634f;
+      float lse2[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) lse2[r] = next_lse[r] * 1.4426950408889634f;
       const bool now_used = mass_used(p, m, lane);
       const int slot = m.valid(sel) ? sel : -1;
       m.next(p);
       sel = m.listed(p, tid);
-      if (m.t != now.t) next_lse = load_lse(m);
+      if (m.t != now.t) load_lse(m);
       float w = 0.f;
       if (now_used) {
         // Warp 0 alone polls; the others sleep at the named barrier
         const bool got = warp != 0 || warp_wait(smem_u32(tfull), tiles & 1, TO, abort_flag);
         if (!named_barrier_and(1, kMassEpilogue, got)) break;
         tc_fence_after();
-        uint32_t za[32], zb[32], zc[16];
+        MassBlock<4> za, zb;
+        MassBlock<2> zc;
         const uint32_t col = tmem_d + lane_off + third * kMassThird;
-        tmem_ld32u(col, za);
-        tmem_ld32u(col + 32, zb);
-        if (third < 2) tmem_ld16u(col + 64, zc);
-        tmem_wait_ld_fence(za);
-        tmem_wait_ld_fence(zb);
-        tmem_wait_ld_fence16(zc);
+        za.load(col);
+        zb.load(col + 32);
+        if (third < 2) zc.load(col + 64);
+        za.wait();
+        zb.wait();
+        if (third < 2) zc.wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(tempty));
         const int n = now.columns(p) - third * kMassThird;
         float* part = sPart + ((tiles & 1) * 4 + quad) * kMassMaxTile + third * kMassThird;
-        if (n > 0) part[lane] = mass_columns(za, p.scale_log2, lse2, lane);
-        if (n > 32) part[32 + lane] = mass_columns(zb, p.scale_log2, lse2, lane);
+        if (n > 0) part[column] = za.sum(p.scale_log2, lse2, lane);
+        if (n > 32) part[32 + column] = zb.sum(p.scale_log2, lse2, lane);
         if (n > 64 && third < 2) {
-          const float v = mass_columns(zc, p.scale_log2, lse2, lane);
-          if (lane < 16) part[64 + lane] = v;
+          const float v = zc.sum(p.scale_log2, lse2, lane);
+          if (lane < 16) part[64 + column] = v;
         }
         named_barrier_sync(2, kMassEpilogue);
         if (tid < kMassMaxTile) {
