@@ -186,15 +186,11 @@ class KvLayout:
         return self.block_table is not None
 
     def c(self) -> KvDescC:
-        d = KvDescC()
-        d.layout = DSA_KV_PAGED if self.paged else DSA_KV_CONTIGUOUS
-        d.batch, d.max_ctx = self.batch, self.max_ctx
-        d.page_size = self.page_size if self.paged else 0
-        d.num_pages = self.num_pages if self.paged else 0
-        d.max_pages = self.block_table.shape[1] if self.paged else 0
-        d.block_table = _ptr(self.block_table).value if self.paged else None
-        d.seqlens = _ptr(self.seqlens).value if self.seqlens is not None else None
-        return d
+        seqlens = None if self.seqlens is None else _ptr(self.seqlens).value
+        if self.block_table is None:
+            return KvDescC(DSA_KV_CONTIGUOUS, self.batch, self.max_ctx, 0, 0, 0, None, seqlens)
+        return KvDescC(DSA_KV_PAGED, self.batch, self.max_ctx, self.page_size, self.num_pages,
+                       self.block_table.shape[1], _ptr(self.block_table).value, seqlens)
 
     @staticmethod
     def of(problem) -> "KvLayout":
@@ -574,77 +570,82 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = Non
     return torch.tensor(theta, dtype=torch.float64, device=device), magnitude
 
 
-def _need(name: str, t: torch.Tensor, dtype, shape, device):
-    """A contiguous CUDA tensor of this type, shape and device (shape None: any)."""
-    if t.dtype != dtype:
+def _need(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
+    """Address of a contiguous tensor of this type, shape (None: any) and device."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return _ptr(t)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _cache_ptrs(kv: KvLayout, kv_cache, k_idx, k_scale, device):
+def _device(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the DSA library must be CUDA tensors")
+    return t.get_device()
+
+
+def _cache_ptrs(kv: KvLayout, kv_cache, k_idx, k_scale, device: int):
     """The three cache arrays of one geometry, checked."""
-    n = ((kv.num_pages, kv.page_size) if kv.paged else (kv.batch, kv.max_ctx))
+    n = (kv.batch, kv.max_ctx) if kv.block_table is None else (kv.num_pages, kv.page_size)
     return (_need("kv_cache", kv_cache, torch.bfloat16, (*n, D_QK), device),
             _need("k_idx", k_idx, torch.uint8, (*n, D_IDX), device),
             _need("k_scale", k_scale, torch.float32, n, device))
 
 
-class _Launch:
-    """The device of the call's tensors made current, and the stream of the call."""
+def _call(name: str, device: int, stream, *args) -> None:
+    """The library call on the device of its tensors, on ``stream`` or that device's
+    current one."""
+    f = getattr(lib(), name)
+    st = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch.cuda.current_device():
+        status = f(*args, st)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, st)
+    if status:
+        raise DSAError(status, name)
 
-    def __init__(self, device: torch.device, stream):
-        if device.type != "cuda":
-            raise ValueError("tensors passed to the DSA library must be CUDA tensors")
-        self.other = None
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.other = torch.cuda.device(device)
-        self.stream = stream
 
-    def __enter__(self):
-        if self.other is not None:
-            self.other.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *a):
-        if self.other is not None:
-            self.other.__exit__(*a)
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A tensor for the call to write, allocated for the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _rope(where, x, positions, freqs, out, rot_begin, interleaved, magnitude, stream):
-    if x.dim() not in (2, 3):
-        raise ValueError("x must be [rows, dim] or [rows, heads, dim]")
     if x.dtype not in _DTYPES:
         raise ValueError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    dev = x.device
-    with _Launch(dev, stream) as st:
-        if out is None:
-            if stream is not None:
-                with torch.cuda.stream(stream):
-                    out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-            else:
-                out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        elif out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
-            raise ValueError("out must have x's shape, type and device")
-        rows, dim = x.shape[0], x.shape[-1]
-        heads = x.shape[1] if x.dim() == 3 else 1
-        if dim > 1 and (x.stride(-1) != 1 or out.stride(-1) != 1):
-            raise ValueError("the last axis of x and out must be contiguous")
-        if freqs.dim() != 1:
-            raise ValueError("freqs must be one-dimensional")
-        d = RopeDescC(_DTYPES[x.dtype], _INTERLEAVED if interleaved else _HALF, heads, dim,
-                      rot_begin, 2 * freqs.shape[0], magnitude, rows, x.stride(0),
-                      x.stride(1) if x.dim() == 3 else dim, out.stride(0),
-                      out.stride(1) if x.dim() == 3 else dim)
-        if heads == 0 or rows == 0:
-            return out
-        _check(getattr(lib(), where)(
-            x.data_ptr(), _need("positions", positions, torch.int32, (rows,), dev),
-            _need("freqs", freqs, torch.float64, None, dev), ctypes.byref(d), out.data_ptr(), st),
-            where)
+    dev = _device(x)
+    if out is None:
+        out = _new(x.shape, x.dtype, x, stream)
+    elif out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != dev:
+        raise ValueError("out must have x's shape, type and device")
+    shape, xs, os = x.shape, x.stride(), out.stride()
+    if len(shape) == 3:
+        rows, heads, dim = shape
+        x_head, out_head = xs[1], os[1]
+    elif len(shape) == 2:
+        (rows, dim), heads = shape, 1
+        x_head = out_head = dim
+    else:
+        raise ValueError("x must be [rows, dim] or [rows, heads, dim]")
+    if dim > 1 and (xs[-1] != 1 or os[-1] != 1):
+        raise ValueError("the last axis of x and out must be contiguous")
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be one-dimensional")
+    d = RopeDescC(_DTYPES[x.dtype], _INTERLEAVED if interleaved else _HALF, heads, dim, rot_begin,
+                  2 * freqs.shape[0], magnitude, rows, xs[0], x_head, os[0], out_head)
+    if heads and rows:
+        _call(where, dev, stream, x.data_ptr(),
+              _need("positions", positions, torch.int32, (rows,), dev),
+              _need("freqs", freqs, torch.float64, None, dev), ctypes.byref(d), out.data_ptr())
     return out
 
 
@@ -674,23 +675,21 @@ def dsa_cache_append(latent_new, k_new, kv_cache, k_idx, k_scale, kv: KvLayout, 
     t goes to the slot of query row t; its rotary position is that slot, or positions[t].
     ``interleaved`` is the pairing of the latent's rope dims, ``idx_interleaved`` that of the
     key's first 64 dims (None: the key is not rotated)."""
-    T, dev = latent_new.shape[0], kv_cache.device
+    T, dev = latent_new.shape[0], _device(kv_cache)
     for name, x, dim in (("latent_new", latent_new, D_QK), ("k_new", k_new, D_IDX)):
-        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape != (T, dim) or x.device != dev:
-            raise ValueError(f"{name} must be a bfloat16 [T, {dim}] tensor on {dev}")
+        if x.dtype is not torch.bfloat16 or x.shape != (T, dim) or x.get_device() != dev:
+            raise ValueError(f"{name} must be a bfloat16 [T, {dim}] tensor on cuda:{dev}")
         if x.stride(1) != 1:
             raise ValueError(f"the last axis of {name} must be contiguous")
-    caches = _cache_ptrs(kv, kv_cache, k_idx, k_scale, dev)
     kvd, qd = kv.c(), _qdesc(T, q_per_seq, rows, q_start)
-    with _Launch(dev, stream) as st:
-        _check(lib().dsa_cache_append(
-            latent_new.data_ptr(), latent_new.stride(0) if T > 1 else D_QK, k_new.data_ptr(),
-            k_new.stride(0) if T > 1 else D_IDX,
-            None if positions is None else _need("positions", positions, torch.int32, (T,), dev),
-            _need("freqs", freqs, torch.float64, (D_ROPE // 2,), dev), float(magnitude),
-            _INTERLEAVED if interleaved else _HALF,
-            _NONE if idx_interleaved is None else _INTERLEAVED if idx_interleaved else _HALF,
-            ctypes.byref(kvd), ctypes.byref(qd), *caches, st), "dsa_cache_append")
+    _call("dsa_cache_append", dev, stream, latent_new.data_ptr(),
+          latent_new.stride(0) if T > 1 else D_QK, k_new.data_ptr(),
+          k_new.stride(0) if T > 1 else D_IDX,
+          None if positions is None else _need("positions", positions, torch.int32, (T,), dev),
+          _need("freqs", freqs, torch.float64, (D_ROPE // 2,), dev), magnitude,
+          _INTERLEAVED if interleaved else _HALF,
+          _NONE if idx_interleaved is None else _INTERLEAVED if idx_interleaved else _HALF,
+          ctypes.byref(kvd), ctypes.byref(qd), *_cache_ptrs(kv, kv_cache, k_idx, k_scale, dev))
 
 
 def dsa_attn_mass_workspace_size(kv: KvLayout, num_q: int, q_per_seq: int, k: int, rows=None,
@@ -699,7 +698,7 @@ def dsa_attn_mass_workspace_size(kv: KvLayout, num_q: int, q_per_seq: int, k: in
     return int(lib().dsa_attn_mass_workspace_size(ctypes.byref(kvd), ctypes.byref(qd), k))
 
 
-def _mass_ptr(name, mass, kv: KvLayout, dev):
+def _mass_ptr(name, mass, kv: KvLayout, dev: int) -> int:
     if mass.dim() != 2 or mass.shape[0] != kv.batch or mass.shape[1] < kv.max_ctx:
         raise ValueError(f"{name} must be [batch, >= max_ctx]")
     return _need(name, mass, torch.float32, None, dev)
@@ -711,25 +710,19 @@ def dsa_attn_mass(q, kv_cache, kv: KvLayout, q_per_seq: int, idx, scale: float, 
     """The head mean of the window's attention weights added to mass [batch, >= max_ctx], by
     slot (include/dsa.h): idx [T, k] and lse [T, 128] as the forward used and wrote them;
     ``workspace`` is a 256-B aligned device tensor (a fresh one when None)."""
-    T, dev = q.shape[0], q.device
-    k = idx.shape[1]
+    T, k, dev = q.shape[0], idx.shape[1], _device(q)
     kvd, qd = kv.c(), _qdesc(T, q_per_seq, rows, q_start)
+    ref, qref = ctypes.byref(kvd), ctypes.byref(qd)
     args = (_need("q", q, torch.bfloat16, (T, HEADS, D_QK), dev),
-            _need("kv_cache", kv_cache, torch.bfloat16, None, dev), ctypes.byref(kvd),
-            ctypes.byref(qd), _need("idx", idx, torch.int32, (T, k), dev), k, float(scale),
+            _need("kv_cache", kv_cache, torch.bfloat16, None, dev), ref, qref,
+            _need("idx", idx, torch.int32, (T, k), dev), k, scale,
             _need("lse", lse, torch.float32, (T, HEADS), dev), _mass_ptr("mass", mass, kv, dev),
             mass.shape[1])
-    with _Launch(dev, stream) as st:
-        if workspace is None:
-            n = max(256, int(lib().dsa_attn_mass_workspace_size(ctypes.byref(kvd),
-                                                                ctypes.byref(qd), k)))
-            if stream is not None:
-                with torch.cuda.stream(stream):
-                    workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-            else:
-                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        nbytes = workspace.numel() * workspace.element_size()
-        _check(lib().dsa_attn_mass(*args, _ptr(workspace), nbytes, st), "dsa_attn_mass")
+    if workspace is None:
+        workspace = _new(max(256, lib().dsa_attn_mass_workspace_size(ref, qref, k)), torch.uint8,
+                         q, stream)
+    _call("dsa_attn_mass", dev, stream, *args, _ptr(workspace),
+          workspace.numel() * workspace.element_size())
     return mass
 
 
@@ -739,20 +732,16 @@ def dsa_evict_select(mass, kv: KvLayout, keep: int, sink: int = 0, recent: int =
                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """The slots that stay when each sequence is trimmed to ``keep`` tokens (include/dsa.h):
     (kept int32 [batch, keep] ascending and padded with -1, new_lens int32 [batch])."""
-    dev = mass.device
-    ptr = _mass_ptr("mass", mass, kv, dev)
+    dev = _device(mass)
+    if kept is None:
+        kept = _new((kv.batch, max(keep, 0)), torch.int32, mass, stream)
+    if new_lens is None:
+        new_lens = _new(kv.batch, torch.int32, mass, stream)
     kvd = kv.c()
-    with _Launch(dev, stream) as st:
-        if kept is None or new_lens is None:
-            with torch.cuda.stream(stream):  # None: the current stream
-                if kept is None:
-                    kept = torch.empty(kv.batch, max(keep, 0), dtype=torch.int32, device=dev)
-                if new_lens is None:
-                    new_lens = torch.empty(kv.batch, dtype=torch.int32, device=dev)
-        _check(lib().dsa_evict_select(
-            ptr, mass.shape[1], ctypes.byref(kvd), keep, sink, recent,
-            _need("kept", kept, torch.int32, (kv.batch, keep), dev),
-            _need("new_lens", new_lens, torch.int32, (kv.batch,), dev), st), "dsa_evict_select")
+    _call("dsa_evict_select", dev, stream, _mass_ptr("mass", mass, kv, dev), mass.shape[1],
+          ctypes.byref(kvd), keep, sink, recent,
+          _need("kept", kept, torch.int32, (kv.batch, keep), dev),
+          _need("new_lens", new_lens, torch.int32, (kv.batch,), dev))
     return kept, new_lens
 
 
@@ -762,30 +751,30 @@ def dsa_cache_compact(kv_cache, k_idx, k_scale, kv: KvLayout, kept, new_lens,
                       stream=None) -> None:
     """Moves the tokens that stay together (include/dsa.h), in place, or into the slots of
     ``dst``: other cache arrays, or the same ones with pages that no source sequence uses."""
-    dev = kv_cache.device
-    src = _cache_ptrs(kv, kv_cache, k_idx, k_scale, dev)
+    dev = _device(kv_cache)
     kvd = kv.c()
-    if dst is None:
-        to, dstd, dst_batch = (dst_kv_cache, dst_k_idx, dst_k_scale), None, kv.batch
-        if any(t is not None for t in (*to, dst_mass)):
-            raise ValueError("dst arrays need a dst layout")
-    else:
-        to, dstd, dst_batch = _cache_ptrs(dst, dst_kv_cache, dst_k_idx, dst_k_scale, dev), \
-            ctypes.byref(dst.c()), dst.batch
-    if dst_batch != kv.batch:
-        raise ValueError("dst must have the source's batch")
     if kept.dim() != 2 or kept.shape[0] != kv.batch:
         raise ValueError("kept must be [batch, keep]")
-    if dst is not None and (mass is None) != (dst_mass is None):
-        raise ValueError("mass and dst_mass go together")
     m = None if mass is None else _mass_ptr("mass", mass, kv, dev)
-    dm = None if dst_mass is None else _mass_ptr("dst_mass", dst_mass, dst, dev)
-    with _Launch(dev, stream) as st:
-        _check(lib().dsa_cache_compact(
-            *src, m, mass.shape[1] if mass is not None else 0, ctypes.byref(kvd),
-            _need("kept", kept, torch.int32, None, dev), kept.shape[1],
-            _need("new_lens", new_lens, torch.int32, (kv.batch,), dev), dstd, *to, dm,
-            dst_mass.shape[1] if dst_mass is not None else 0, st), "dsa_cache_compact")
+    dm, dstd = None, None
+    if dst is None:
+        to = (dst_kv_cache, dst_k_idx, dst_k_scale)
+        if to != (None, None, None) or dst_mass is not None:
+            raise ValueError("dst arrays need a dst layout")
+    else:
+        if dst.batch != kv.batch:
+            raise ValueError("dst must have the source's batch")
+        if (mass is None) != (dst_mass is None):
+            raise ValueError("mass and dst_mass go together")
+        to = _cache_ptrs(dst, dst_kv_cache, dst_k_idx, dst_k_scale, dev)
+        dm = None if dst_mass is None else _mass_ptr("dst_mass", dst_mass, dst, dev)
+        dstc = dst.c()
+        dstd = ctypes.byref(dstc)
+    _call("dsa_cache_compact", dev, stream, *_cache_ptrs(kv, kv_cache, k_idx, k_scale, dev), m,
+          0 if m is None else mass.shape[1], ctypes.byref(kvd),
+          _need("kept", kept, torch.int32, None, dev), kept.shape[1],
+          _need("new_lens", new_lens, torch.int32, (kv.batch,), dev), dstd, *to, dm,
+          0 if dm is None else dst_mass.shape[1])
 
 
 def dsa_get_device_error(stream=None) -> int:
