@@ -399,7 +399,7 @@ typedef enum { DSA_ROPE_HALF = 0, DSA_ROPE_INTERLEAVED = 1, DSA_ROPE_NONE = 2 } 
 typedef struct {
   int32_t dtype;          /* dsa_dtype_t of x and out                                   */
   int32_t layout;         /* DSA_ROPE_HALF or DSA_ROPE_INTERLEAVED                      */
-  int32_t heads, dim;
+  int32_t heads, dim;     /* heads <= 65535, dim <= 32768                               */
   int32_t rot_begin;      /* first rotated dim of a head                                */
   int32_t rot_dim;        /* rotated dims: even, 2..512, rot_begin + rot_dim <= dim     */
   float magnitude;        /* factor on the rotated dims (1, or YaRN's attention factor) */

@@ -837,8 +837,8 @@ dsa_status_t launch_rope(const void* x, const int32_t* positions, const double* 
   if (d->num_rows < 0 || d->heads < 1 || d->dim < 1 || d->rot_begin < 0 || d->rot_dim < 2 ||
       d->rot_dim % 2 || d->rot_begin > d->dim - d->rot_dim)
     return DSA_ERR_INVALID_ARG;
-  if (d->rot_dim > kRopeMaxRot || d->num_rows >= (1ll << 31) || d->dim > (1 << 20) ||
-      d->heads > (1 << 20))
+  if (d->rot_dim > kRopeMaxRot || d->num_rows >= (1ll << 31) || d->dim > kRopeMaxDim ||
+      d->heads > 65535)
     return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!(std::fabs(d->magnitude) < 1e30f)) return DSA_ERR_INVALID_ARG;
   if (d->num_rows == 0) return DSA_OK;
@@ -876,33 +876,40 @@ dsa_status_t launch_rope(const void* x, const int32_t* positions, const double* 
   p.heads = d->heads;
   p.half = d->rot_dim / 2;
   p.rot_begin = d->rot_begin;
-  p.dim = d->dim;
-  p.copy = !in_place && d->dim > d->rot_dim;
   p.magnitude = d->magnitude;
   p.sign = transposed ? -1.f : 1.f;
   const bool inter = d->layout == DSA_ROPE_INTERLEAVED;
   // 16-byte accesses where every row and run starts on a 16-byte boundary
   const int v = 16 / es;
   bool wide = !((xa | oa) & 15) && d->rot_begin % v == 0 &&
-              (inter ? d->rot_dim : p.half) % v == 0 && (!p.copy || d->dim % v == 0);
+              (inter ? d->rot_dim : p.half) % v == 0 && (in_place || d->dim % v == 0);
   for (int i = 0; i < 4; ++i)
     wide = wide && ((i & 1 ? d->heads : d->num_rows) == 1 || strides[i] % v == 0);
   const int vec = wide ? v : 1;
-  const int pairs = inter ? std::max(1, vec / 2) : vec;
-  const int64_t units = p.half / pairs + (p.copy ? (d->dim - d->rot_dim) / vec : 0);
-  const int64_t total = units * d->heads * d->num_rows;
-  const int64_t target = total >= 1184 * 1024 ? 1024 : kRopeThreads;
-  const int64_t per_row = units * d->heads;
-  p.rows_per_block = (int)std::max<int64_t>(
-      1, std::min({target / per_row, (int64_t)kRopeMaxRows, (int64_t)(kRopeTable / p.half)}));
-  p.heads_per_block = (int)std::max<int64_t>(1, std::min<int64_t>(d->heads, target / units));
-  const int64_t gx = (d->num_rows + p.rows_per_block - 1) / p.rows_per_block;
-  int64_t gy = (d->heads + p.heads_per_block - 1) / p.heads_per_block;
-  if (gy > 65535) {
-    p.heads_per_block = (d->heads + 65534) / 65535;
-    gy = (d->heads + p.heads_per_block - 1) / p.heads_per_block;
+  const bool two = !inter || vec == 1;
+  const int run = two ? 2 * vec : vec;  // dims of a unit
+  p.copied = in_place ? 0 : d->dim - d->rot_dim;
+  p.rot_units = d->rot_dim / run;
+  p.units = p.rot_units + (p.copied + run - 1) / run;
+  p.row_blocks = (p.units + kRopeThreads - 1) / kRopeThreads;
+  if (d->num_rows * p.row_blocks >= (1ll << 31)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  // A thread takes eight heads once that fills the GPU (eight blocks an SM), else one. Few
+  // heads: a block takes several rows.
+  const int most = 8;
+  const int64_t total = (int64_t)p.units * d->heads * d->num_rows;
+  p.turns = total >= 8ll * num_sms() * kRopeThreads * most ? most : 1;
+  const int side = (d->heads + p.turns - 1) / p.turns;  // heads side by side, at most
+  p.block_rows = 1;
+  p.block_units = std::min(p.units, kRopeThreads);
+  if (p.row_blocks == 1) {
+    p.block_rows = (int)std::max<int64_t>(
+        1, std::min<int64_t>(d->num_rows, kRopeThreads / ((int64_t)p.units * side)));
+    p.block_units = p.units * p.block_rows;
   }
-  const dim3 grid((unsigned)gx, (unsigned)gy);
+  const int heads_per_block = kRopeThreads / p.block_units * p.turns;
+  const dim3 grid((unsigned)(p.row_blocks > 1 ? d->num_rows * p.row_blocks
+                                              : (d->num_rows + p.block_rows - 1) / p.block_rows),
+                  (unsigned)((d->heads + heads_per_block - 1) / heads_per_block));
   auto go = [&](auto kernel) { kernel<<<grid, kRopeThreads, 0, stream>>>(p); };
   if (d->dtype == DSA_FP32) {
     if (inter) wide ? go(rope_kernel<float, 4, true>) : go(rope_kernel<float, 1, true>);
@@ -946,8 +953,10 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
 }
 
 // ---- compact -----------------------------------------------------------------------
-// CTAs per slice: about three on every SM. In place they form a cluster (of at most
-// eight, the portable size), which moves its chunks in order.
+// CTAs per slice. Into other pages about twelve for every SM (three are resident): 48
+// sequences of 8192 kept tokens took 195 us with three for every SM, 185 with twelve. In
+// place they form a cluster (of at most eight, the portable size), which moves its chunks
+// in order, and six for every SM are enough (168 us; 172 with twelve).
 dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t attr_err = once_per_device(once, [] {
@@ -959,7 +968,7 @@ dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStre
   });
   if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
   const int64_t chunks = (p.keep + kCompactRows - 1) / kCompactRows;
-  const int64_t fill = (3 * num_sms() + (int64_t)batch * kCompactSlices - 1) /
+  const int64_t fill = ((in_place ? 6 : 12) * num_sms() + (int64_t)batch * kCompactSlices - 1) /
                        ((int64_t)batch * kCompactSlices);
   p.splits = (int)std::min(chunks, fill);
   if (in_place)

@@ -8,9 +8,13 @@
 //
 // The kernel moves 2 x (row bytes) and computes three flops a dim, so memory bounds it.
 // The angle is formed in fp64 turns and reduced to [-1/2, 1/2] before it becomes fp32:
-// at position 10^6 an fp32 product would be off by 0.06 rad. That costs one fp64
-// multiplication per (row, pair); every head of the row reads the sine and cosine from
-// shared memory.
+// at position 10^6 an fp32 product would be off by 0.06 rad. A thread owns one unit (a run
+// of dims with their partners, or as many dims to copy) of one row and takes it through
+// several heads with its sines and cosines in registers; the block forms each of them once,
+// in shared memory, while the first loads are on their way. What is left is bytes in
+// flight: five blocks an SM whose threads have two runs of 16 B under way each carry 8192
+// rows of 64 bf16 heads (half of 128 dims rotated) in 55 us, four blocks with four runs in
+// 63, three in 67.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,9 +25,8 @@
 namespace dsa {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxRows = 32;     // rows of one block
 constexpr int kRopeMaxRot = 512;     // rotated dims of a head
-constexpr int kRopeTable = 2048;     // (row, pair) entries of one block's table, 16 KB
+constexpr int kRopeMaxDim = 32768;
 
 struct RopeParams {
   const void* x;
@@ -32,9 +35,14 @@ struct RopeParams {
   const double* freqs;       // [half] radians per position
   int64_t x_row, x_head, o_row, o_head;  // strides in elements
   int64_t rows;
-  int32_t heads, half, rot_begin, dim;
-  int32_t rows_per_block, heads_per_block;
-  int32_t copy;              // dims outside the rotated part are copied
+  int32_t heads, half, rot_begin;
+  int32_t copied;            // dims of a head to copy (0 in place)
+  int32_t rot_units, units;  // of a head: rotated, and with those to copy
+  int32_t row_blocks;        // blocks that share a row's units (1: a block takes whole rows)
+  int32_t block_rows;        // rows of a block (row_blocks = 1)
+  int32_t block_units;       // (row, unit) pairs of a block; kRopeThreads / block_units heads
+                             // go side by side
+  int32_t turns;             // heads of a thread
   float magnitude, sign;     // sign = -1: transposed
 };
 
@@ -68,76 +76,105 @@ struct alignas(V * sizeof(T)) RopeVec {
   T v[V];
 };
 
-// A unit is what one thread does at once: V dims of the rotated part with their
-// partners (interleaved: one run of max(V, 2) dims; half layout: two runs of V), or V
-// dims to copy.
+// A unit of a head: one run of V dims (interleaved, V > 1), else two runs of V dims, `gap`
+// apart. Rotated: a run of pairs, or the firsts and seconds of V pairs.
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-  using Vec = RopeVec<T, V>;
-  constexpr int kPairs = kInterleaved ? (V > 1 ? V / 2 : 1) : V;
-  __shared__ float2 table[kRopeTable];
-  const int64_t row0 = (int64_t)blockIdx.x * p.rows_per_block;
-  const int nrows = (int)min((int64_t)p.rows_per_block, p.rows - row0);
-  const int h0 = blockIdx.y * p.heads_per_block;
-  const int nheads = min(p.heads_per_block, p.heads - h0);
-  for (int i = threadIdx.x; i < nrows * p.half; i += kRopeThreads) {
-    const int r = i / p.half, j = i - r * p.half;
-    float2 t = rope_turn(__ldg(p.positions + row0 + r), __ldg(p.freqs + j), p.magnitude);
+struct RopeUnit {
+  static constexpr bool kTwo = !kInterleaved || V == 1;
+  static constexpr int kPairs = kTwo ? V : V / 2;
+  RopeVec<T, V> lo, hi;
+  __device__ __forceinline__ void load(const T* x, int gap, bool two) {
+    lo = *reinterpret_cast<const RopeVec<T, V>*>(x);
+    if (kTwo && two) hi = *reinterpret_cast<const RopeVec<T, V>*>(x + gap);
+  }
+  __device__ __forceinline__ void store(T* out, int gap, bool two) const {
+    *reinterpret_cast<RopeVec<T, V>*>(out) = lo;
+    if (kTwo && two) *reinterpret_cast<RopeVec<T, V>*>(out + gap) = hi;
+  }
+  __device__ __forceinline__ void turn(const float2 (&t)[kPairs]) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      T& first = kTwo ? lo.v[j] : lo.v[(2 * j) % V];
+      T& second = kTwo ? hi.v[j] : lo.v[(2 * j + 1) % V];
+      const float a = rope_to_float(first), b = rope_to_float(second);
+      first = rope_from_float<T>(a * t[j].x - b * t[j].y);
+      second = rope_from_float<T>(a * t[j].y + b * t[j].x);
+    }
+  }
+};
+
+template <typename T, int V, bool kInterleaved>
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const RopeParams p) {
+  using Unit = RopeUnit<T, V, kInterleaved>;
+  constexpr int kPairs = Unit::kPairs;
+  constexpr int kRun = Unit::kTwo ? 2 * V : V;     // dims of a unit
+  constexpr int kHeads = Unit::kTwo ? 1 : 2;       // in flight: two runs of a thread
+  const int slot = threadIdx.x / p.block_units, c = threadIdx.x - slot * p.block_units;
+  const int slots = kRopeThreads / p.block_units;
+  int64_t row;
+  int u;
+  if (p.row_blocks == 1) {
+    const int r = c / p.units;
+    row = (int64_t)blockIdx.x * p.block_rows + r;
+    u = c - r * p.units;
+  } else {
+    row = blockIdx.x / p.row_blocks;
+    u = (int)(blockIdx.x - row * p.row_blocks) * p.block_units + c;
+  }
+  int h = (int)blockIdx.y * p.turns * slots + slot;
+  const int end = min(p.heads, h - slot + p.turns * slots);
+  const bool active = slot < slots && row < p.rows && u < p.units && h < end;
+  const bool turned = active && u < p.rot_units;
+  int d, gap;
+  bool two = true;
+  if (turned) {
+    d = p.rot_begin + u * (kInterleaved ? kRun : V);
+    gap = kInterleaved ? 1 : p.half;
+  } else {  // dims to copy, numbered without the rotated part: a run of each half of them
+    const int e = (u - p.rot_units) * V, next = e + (p.units - p.rot_units) * V;
+    auto dim = [&](int i) { return i < p.rot_begin ? i : i + 2 * p.half; };
+    d = dim(e);
+    gap = dim(next) - d;
+    two = next < p.copied;
+  }
+  const T* x = reinterpret_cast<const T*>(p.x) + row * p.x_row + d;
+  T* out = reinterpret_cast<T*>(p.out) + row * p.o_row + d;
+  Unit e[kHeads];
+  auto load = [&] {
+#pragma unroll
+    for (int j = 0; j < kHeads; ++j)
+      if (h + j * slots < end) e[j].load(x + (h + j * slots) * p.x_head, gap, two);
+  };
+  if (active) load();
+  // block_rows * half <= kRopeThreads * kPairs entries: a row has half / kPairs units or more
+  __shared__ float2 table[kRopeThreads * kPairs];
+  const int64_t row0 = p.row_blocks == 1 ? (int64_t)blockIdx.x * p.block_rows : row;
+  const int entries = (int)min((int64_t)p.block_rows, p.rows - row0) * p.half;
+  for (int i = threadIdx.x; i < entries; i += kRopeThreads) {
+    const int r = i / p.half;
+    float2 t = rope_turn(__ldg(p.positions + row0 + r), __ldg(p.freqs + i - r * p.half),
+                         p.magnitude);
     t.y *= p.sign;
     table[i] = t;
   }
   __syncthreads();
-  const int rot_units = p.half / kPairs;
-  const int units = rot_units + (p.copy ? (p.dim - 2 * p.half) / V : 0);
-  const int total = nrows * nheads * units;
-  const T* x = reinterpret_cast<const T*>(p.x);
-  T* out = reinterpret_cast<T*>(p.out);
-  for (int i = threadIdx.x; i < total; i += kRopeThreads) {
-    const int rh = i / units, u = i - rh * units;
-    const int r = rh / nheads, h = h0 + rh - r * nheads;
-    const T* xs = x + (row0 + r) * p.x_row + h * p.x_head;
-    T* os = out + (row0 + r) * p.o_row + h * p.o_head;
-    if (u >= rot_units) {
-      int d = (u - rot_units) * V;
-      if (d >= p.rot_begin) d += 2 * p.half;
-      *reinterpret_cast<Vec*>(os + d) = *reinterpret_cast<const Vec*>(xs + d);
-      continue;
-    }
-    const float2* t = table + r * p.half + u * kPairs;
-    if constexpr (kInterleaved) {
-      const int d = p.rot_begin + u * 2 * kPairs;
-      T e[2 * kPairs];
-      if constexpr (V > 1) {
-        *reinterpret_cast<Vec*>(e) = *reinterpret_cast<const Vec*>(xs + d);
-      } else {
-        e[0] = xs[d];
-        e[1] = xs[d + 1];
-      }
+  if (!active) return;
+  float2 t[kPairs];
+  if (turned) {
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) {
-        const float a = rope_to_float(e[2 * j]), b = rope_to_float(e[2 * j + 1]);
-        e[2 * j] = rope_from_float<T>(a * t[j].x - b * t[j].y);
-        e[2 * j + 1] = rope_from_float<T>(a * t[j].y + b * t[j].x);
-      }
-      if constexpr (V > 1) {
-        *reinterpret_cast<Vec*>(os + d) = *reinterpret_cast<const Vec*>(e);
-      } else {
-        os[d] = e[0];
-        os[d + 1] = e[1];
-      }
-    } else {
-      const int d = p.rot_begin + u * V;
-      Vec lo = *reinterpret_cast<const Vec*>(xs + d);
-      Vec hi = *reinterpret_cast<const Vec*>(xs + d + p.half);
+    for (int j = 0; j < kPairs; ++j) t[j] = table[(int)(row - row0) * p.half + u * kPairs + j];
+  }
+  while (true) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float a = rope_to_float(lo.v[j]), b = rope_to_float(hi.v[j]);
-        lo.v[j] = rope_from_float<T>(a * t[j].x - b * t[j].y);
-        hi.v[j] = rope_from_float<T>(a * t[j].y + b * t[j].x);
+    for (int j = 0; j < kHeads; ++j) {
+      if (h + j * slots < end) {
+        if (turned) e[j].turn(t);
+        e[j].store(out + (h + j * slots) * p.o_head, gap, two);
       }
-      *reinterpret_cast<Vec*>(os + d) = lo;
-      *reinterpret_cast<Vec*>(os + d + p.half) = hi;
     }
+    h += kHeads * slots;
+    if (h >= end) break;
+    load();
   }
 }
 

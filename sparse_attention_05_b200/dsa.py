@@ -545,8 +545,7 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = Non
       "ntk"     the same for base * factor^(rot_dim / (rot_dim - 2))
       "yarn"    g_i theta_i + (1 - g_i) theta_i / factor, g_i rising linearly from 0 at
                 beta_slow to 1 at beta_fast turns over original_ctx positions, and the
-                magnitude 0.1 ln(factor) + 1 (YaRN, arXiv 2309.00071, section 3.2 and
-                equation 22)
+                magnitude 0.1 ln(factor) + 1 (YaRN, arXiv 2309.00071, section 3)
     Any other schedule is a tensor of one's own."""
     if rot_dim < 2 or rot_dim % 2 or base <= 0 or factor <= 0 or original_ctx < 1:
         raise ValueError("rope_freqs: rot_dim must be even and base, factor, original_ctx positive")
@@ -589,9 +588,26 @@ def _device(t: torch.Tensor) -> int:
     return t.get_device()
 
 
+def _kv_desc(kv: KvLayout, device: int, q_start: Optional[torch.Tensor] = None) -> KvDescC:
+    """kv.c() with its tensors' types, sizes and device checked (and q_start's size)."""
+    if kv.seqlens is not None:
+        _need("seqlens", kv.seqlens, torch.int32, (kv.batch,), device)
+    if kv.block_table is not None:
+        if kv.block_table.dim() != 2 or kv.block_table.shape[0] != kv.batch:
+            raise ValueError("block_table must be [batch, max_pages]")
+        _need("block_table", kv.block_table, torch.int32, None, device)
+    if q_start is not None:
+        _need("q_start", q_start, torch.int32, (kv.batch + 1,), device)
+    return kv.c()
+
+
+def _rows_shape(kv: KvLayout):
+    return (kv.batch, kv.max_ctx) if kv.block_table is None else (kv.num_pages, kv.page_size)
+
+
 def _cache_ptrs(kv: KvLayout, kv_cache, k_idx, k_scale, device: int):
     """The three cache arrays of one geometry, checked."""
-    n = (kv.batch, kv.max_ctx) if kv.block_table is None else (kv.num_pages, kv.page_size)
+    n = _rows_shape(kv)
     return (_need("kv_cache", kv_cache, torch.bfloat16, (*n, D_QK), device),
             _need("k_idx", k_idx, torch.uint8, (*n, D_IDX), device),
             _need("k_scale", k_scale, torch.float32, n, device))
@@ -681,7 +697,7 @@ def dsa_cache_append(latent_new, k_new, kv_cache, k_idx, k_scale, kv: KvLayout, 
             raise ValueError(f"{name} must be a bfloat16 [T, {dim}] tensor on cuda:{dev}")
         if x.stride(1) != 1:
             raise ValueError(f"the last axis of {name} must be contiguous")
-    kvd, qd = kv.c(), _qdesc(T, q_per_seq, rows, q_start)
+    kvd, qd = _kv_desc(kv, dev, q_start), _qdesc(T, q_per_seq, rows, q_start)
     _call("dsa_cache_append", dev, stream, latent_new.data_ptr(),
           latent_new.stride(0) if T > 1 else D_QK, k_new.data_ptr(),
           k_new.stride(0) if T > 1 else D_IDX,
@@ -711,10 +727,10 @@ def dsa_attn_mass(q, kv_cache, kv: KvLayout, q_per_seq: int, idx, scale: float, 
     slot (include/dsa.h): idx [T, k] and lse [T, 128] as the forward used and wrote them;
     ``workspace`` is a 256-B aligned device tensor (a fresh one when None)."""
     T, k, dev = q.shape[0], idx.shape[1], _device(q)
-    kvd, qd = kv.c(), _qdesc(T, q_per_seq, rows, q_start)
+    kvd, qd = _kv_desc(kv, dev, q_start), _qdesc(T, q_per_seq, rows, q_start)
     ref, qref = ctypes.byref(kvd), ctypes.byref(qd)
     args = (_need("q", q, torch.bfloat16, (T, HEADS, D_QK), dev),
-            _need("kv_cache", kv_cache, torch.bfloat16, None, dev), ref, qref,
+            _need("kv_cache", kv_cache, torch.bfloat16, (*_rows_shape(kv), D_QK), dev), ref, qref,
             _need("idx", idx, torch.int32, (T, k), dev), k, scale,
             _need("lse", lse, torch.float32, (T, HEADS), dev), _mass_ptr("mass", mass, kv, dev),
             mass.shape[1])
@@ -737,7 +753,7 @@ def dsa_evict_select(mass, kv: KvLayout, keep: int, sink: int = 0, recent: int =
         kept = _new((kv.batch, max(keep, 0)), torch.int32, mass, stream)
     if new_lens is None:
         new_lens = _new(kv.batch, torch.int32, mass, stream)
-    kvd = kv.c()
+    kvd = _kv_desc(kv, dev)
     _call("dsa_evict_select", dev, stream, _mass_ptr("mass", mass, kv, dev), mass.shape[1],
           ctypes.byref(kvd), keep, sink, recent,
           _need("kept", kept, torch.int32, (kv.batch, keep), dev),
@@ -752,7 +768,7 @@ def dsa_cache_compact(kv_cache, k_idx, k_scale, kv: KvLayout, kept, new_lens,
     """Moves the tokens that stay together (include/dsa.h), in place, or into the slots of
     ``dst``: other cache arrays, or the same ones with pages that no source sequence uses."""
     dev = _device(kv_cache)
-    kvd = kv.c()
+    kvd = _kv_desc(kv, dev)
     if kept.dim() != 2 or kept.shape[0] != kv.batch:
         raise ValueError("kept must be [batch, keep]")
     m = None if mass is None else _mass_ptr("mass", mass, kv, dev)
@@ -768,7 +784,7 @@ def dsa_cache_compact(kv_cache, k_idx, k_scale, kv: KvLayout, kept, new_lens,
             raise ValueError("mass and dst_mass go together")
         to = _cache_ptrs(dst, dst_kv_cache, dst_k_idx, dst_k_scale, dev)
         dm = None if dst_mass is None else _mass_ptr("dst_mass", dst_mass, dst, dev)
-        dstc = dst.c()
+        dstc = _kv_desc(dst, dev)
         dstd = ctypes.byref(dstc)
     _call("dsa_cache_compact", dev, stream, *_cache_ptrs(kv, kv_cache, k_idx, k_scale, dev), m,
           0 if m is None else mass.shape[1], ctypes.byref(kvd),
