@@ -24,6 +24,7 @@ constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictGroup = kEvictBins / kEvictWarps;  // bins of one partial sum
+constexpr int kEvictLoads = 16;           // of a thread, in flight
 constexpr int kEvictMaxSplits = 8;
 constexpr int kEvictMaxKeys = 45056;      // keys a CTA holds in shared memory (176 KB)
 constexpr int kEvictMaxCtx = 1 << 22;     // two bits a slot fit in shared memory up to here
@@ -202,15 +203,15 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
   };
   for (int i = tid; i < 4 * kEvictBins; i += kEvictThreads) (&sh.hist[0][0])[i] = 0;
   __syncthreads();
-  for (int i0 = warp * 32; i0 < count; i0 += kEvictThreads * 8) {
-    float m[8];  // eight loads of a thread in flight
+  for (int i0 = warp * 32; i0 < count; i0 += kEvictThreads * kEvictLoads) {
+    float m[kEvictLoads];  // in flight at once
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kEvictLoads; ++j) {
       const int i = i0 + j * kEvictThreads + lane;
       m[j] = i < count ? __ldg(mass + i) : 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kEvictLoads; ++j) {
       const int i = i0 + j * kEvictThreads + lane;
       const uint32_t key = evict_key(m[j]);
       if (p.hold && i < count) keys[i] = key;
@@ -303,15 +304,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
       g += a, e += c;
     }
     for (int over = ne - max(0, left - be); over > 0 && at; --over) at &= ~(0x80000000u >> __clz(at));
-    const uint32_t word = above | at;
-    const int place = p.sink + bg + min(be, left);
-#pragma unroll 4
-    for (int j = 0; j < 32; ++j) {
-      const uint32_t m = __shfl_sync(0xffffffffu, word, j);
-      const int at_j = __shfl_sync(0xffffffffu, place, j);
-      if ((m >> lane) & 1)
-        kept[at_j + __popc(m & ((1u << lane) - 1))] = begin + (w0 + warp * 32 + j) * 32 + lane;
-    }
+    // a thread writes its own word's slots: neighbours write next to each other
+    int32_t* to = kept + p.sink + bg + min(be, left);
+    for (uint32_t word = above | at; word; word &= word - 1)
+      *to++ = begin + w * 32 + __ffs(word) - 1;
     __syncthreads();
   }
   cluster_sync_all();  // no CTA leaves while another still reads its shared memory
