@@ -527,20 +527,41 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   }
 }
 
-// Few rows: one CTA adds a sequence's rows in order.
-__global__ void __launch_bounds__(512) mass_add_rows_kernel(const __grid_constant__ MassParams p) {
+// Few rows: one CTA adds a sequence's rows in order, four entries of a thread at a time; the
+// next ones are loaded before the barrier between two rows.
+constexpr int kMassAddThreads = 512;
+__global__ void __launch_bounds__(kMassAddThreads)
+    mass_add_rows_kernel(const __grid_constant__ MassParams p) {
   const int b = blockIdx.x;
   const SeqRows R = seq_rows(p.q_start, p.seqlens, b, p.q_per_seq, p.num_q, p.max_ctx);
   if (!R.ok) return;
   const int last = min(p.row_begin + p.row_count, R.q_len);
   float* mass = p.mass + (int64_t)b * p.mass_ld;
+  int sel[4];
+  float w[4];
+  auto load = [&](int qi, int e0) {
+    const int32_t* idx = p.idx + (R.t0 + qi) * p.k;
+    const float* row = p.p_out + ((int64_t)b * p.row_count + qi - p.row_begin) * p.k;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = e0 + j * kMassAddThreads + threadIdx.x;
+      sel[j] = qi < last && e < p.k ? __ldg(idx + e) : -1;
+      w[j] = qi < last && e < p.k ? __ldg(row + e) : 0.f;
+    }
+  };
+  load(p.row_begin, 0);
   for (int qi = p.row_begin; qi < last; ++qi) {
     const int pos = R.seqlen - R.q_len + qi;
-    const int32_t* idx = p.idx + (R.t0 + qi) * p.k;
-    const float* w = p.p_out + ((int64_t)b * p.row_count + qi - p.row_begin) * p.k;
-    for (int e = threadIdx.x; e < p.k; e += blockDim.x) {
-      const int sel = __ldg(idx + e);
-      if (sel >= 0 && sel <= pos) atomicAdd(mass + sel, w[e]);
+    for (int e0 = 0; e0 < p.k;) {
+      int s[4];
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] = sel[j], v[j] = w[j];
+      e0 += 4 * kMassAddThreads;
+      e0 < p.k ? load(qi, e0) : load(qi + 1, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (s[j] >= 0 && s[j] <= pos) atomicAdd(mass + s[j], v[j]);
     }
     __syncthreads();
   }

@@ -1058,7 +1058,7 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
   attn_mass_kernel<<<grid, kMassThreads, kMassSmemBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (few)
-    mass_add_rows_kernel<<<(unsigned)g.batch, 512, 0, stream>>>(p);
+    mass_add_rows_kernel<<<(unsigned)g.batch, kMassAddThreads, 0, stream>>>(p);
   else
     mass_add_sums_kernel<<<dim3((unsigned)((g.max_ctx + 255) / 256), (unsigned)g.batch), 256, 0,
                            stream>>>(p);
