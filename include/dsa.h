@@ -455,8 +455,8 @@ DSA_API dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_str
  *         k in [1, 2^20]
  *  mass   fp32 [batch][mass_ld], mass_ld >= max_ctx, by slot; added to
  *  workspace  device, 256-byte aligned, dsa_attn_mass_workspace_size() bytes; written
- *         during the call (stream order), nothing kept in it. With more than 8 rows a
- *         sequence the rows are summed in units of 2^-40. */
+ *         during the call (stream order), nothing kept in it. Many rows (for the
+ *         caches' size) are summed in units of 2^-40, a few in fp32. */
 DSA_API size_t dsa_attn_mass_workspace_size(const dsa_kv_desc_t* kv, const dsa_q_desc_t* q,
                                             int32_t k);
 DSA_API dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const dsa_kv_desc_t* kv,

@@ -990,12 +990,18 @@ dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStre
 }
 
 // ---- attention mass ----------------------------------------------------------------
-// Rows of a sequence up to which its rows' weights are added one row after another.
-constexpr int kMassFewRows = 8;
+// Whether a sequence's rows are added one after another (0.85 us each, one CTA a sequence) or
+// as integers (24 B a slot zeroed, read and added, at 2.5 TB/s, and 2 us of launches): the
+// cheaper by these measured costs. 128 x 2 rows of 32K slots take 133 us the first way and
+// 168 the second, 1 x 16 rows 39 and 25.
+bool mass_few_rows(const Geometry& g, int k) {
+  return (int64_t)g.row_count * ((k + 4 * kMassAddThreads - 1) / (4 * kMassAddThreads)) * 88000 <=
+         200000 + (int64_t)g.batch * g.max_ctx;
+}
 
 size_t mass_workspace(const Geometry& g, int k) {
-  return g.row_count <= kMassFewRows ? align256((size_t)g.batch * g.row_count * k * 4)
-                                     : align256((size_t)g.batch * g.max_ctx * 8);
+  return mass_few_rows(g, k) ? align256((size_t)g.batch * g.row_count * k * 4)
+                             : align256((size_t)g.batch * g.max_ctx * 8);
 }
 
 dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometry& g,
@@ -1016,7 +1022,7 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
   p.block_table = g.block_table;
   p.seqlens = g.seqlens;
   p.q_start = g.q_start;
-  const bool few = g.row_count <= kMassFewRows;
+  const bool few = mass_few_rows(g, k);
   if (few)
     p.p_out = reinterpret_cast<float*>(workspace);
   else

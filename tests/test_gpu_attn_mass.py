@@ -88,7 +88,7 @@ def _idx(p, k, seed):
     return _lists(p.num_q, oracle_args(p)["q_pos"], k, seed)
 
 
-@pytest.mark.parametrize("k", [1, 100, 128, 129, 700])
+@pytest.mark.parametrize("k", [1, 100, 128, 129, 225, 700, 2000])
 def test_decode(k):
     p = synth.decode(batch=3, ctx=900, q_per_seq=1, seed=70 + k)
     mass0, mass = _check(p, _idx(p, k, k))
@@ -102,7 +102,7 @@ def test_paged_two_rows_and_short_context():
     _check(p, _idx(p, 256, 1))
 
 
-@pytest.mark.parametrize("rows", [8, 9, 40])
+@pytest.mark.parametrize("rows", [2, 3, 8, 40])
 def test_few_and_many_rows_of_a_sequence(rows):
     """On both sides of the border between the two ways of summing."""
     p = synth.ragged([300, 200], [rows, rows // 2], seed=82 + rows)
@@ -197,3 +197,49 @@ def test_own_workspace_other_stream_and_graph():
             dsa.dsa_attn_mass(q, g.kv, lay, rows, li, p.scale, lse, mass)
         graph.replay()
         assert torch.equal(mass, want)
+
+
+def test_the_two_ways_of_summing_agree():
+    """One batch both ways: the window of all its rows at once (integers), and row by row (each
+    call adds a few rows in fp32): apart by at most 2^-41 and one fp32 step per entry."""
+    p = synth.ragged([300, 200], [12, 12], seed=89)
+    idx = _idx(p, 100, 11)
+    g = p.to(DEV)
+    li = torch.from_numpy(idx).cuda()
+    lay = dsa.KvLayout.of(g)
+    lse = torch.full((p.num_q, 128), 6.0, device=DEV)
+    sizes = [dsa.dsa_attn_mass_workspace_size(lay, p.num_q, 12, 100, rows=w, q_start=g.q_start)
+             for w in (None, (0, 1))]
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    assert sizes == [up(2 * p.max_ctx * 8), up(2 * 100 * 4)]  # the two workspaces
+    whole, single = torch.zeros(2, p.max_ctx, device=DEV), torch.zeros(2, p.max_ctx, device=DEV)
+    dsa.dsa_attn_mass(g.q, g.kv, lay, 12, li, p.scale, lse, whole, q_start=g.q_start)
+    for i in range(12):
+        dsa.dsa_attn_mass(g.q, g.kv, lay, 12, li, p.scale, lse, single, rows=(i, 1),
+                          q_start=g.q_start)
+    assert torch.all((whole - single).abs() <= 12 * 2.0 ** -41 + 13 * 2.0 ** -24 * single)
+
+
+def test_long_prefill_agrees_with_its_windows():
+    """So many rows that a CTA takes whole ones in turn, some of them with tiles without an
+    entry, against windows of a hundred rows (runs of tiles): integer sums of the same weights,
+    added to fp32 once and 25 times."""
+    L, k = 2500, 300
+    g = torch.Generator(device=DEV).manual_seed(90)
+    q = (torch.randn(L, 128, 576, device=DEV, generator=g) * 2).bfloat16()
+    kv = (torch.randn(1, L, 576, device=DEV, generator=g) * 0.5).bfloat16()
+    r = torch.rand(L, L, device=DEV, generator=g)
+    at = torch.arange(L, device=DEV)
+    v, i = r.masked_fill(at > at[:, None], -1.0).topk(k, dim=1)
+    i = torch.where(v >= 0, i, L).sort(dim=1).values
+    idx = torch.where(i < L, i, -1).int()
+    lay = dsa.KvLayout(1, L)
+    out, lse = dsa.dsa_sparse_mla_fwd(q, kv, lay, L, idx, 576 ** -0.5)
+    whole, parts = torch.zeros(1, L, device=DEV), torch.zeros(1, L, device=DEV)
+    dsa.dsa_attn_mass(q, kv, lay, L, idx, 576 ** -0.5, lse, whole)
+    for w in range(0, L, 100):
+        dsa.dsa_attn_mass(q, kv, lay, L, idx, 576 ** -0.5, lse, parts, rows=(w, 100))
+    torch.cuda.synchronize()
+    assert dsa.dsa_get_device_error() == 0
+    assert torch.all((whole - parts).abs() <= 27 * 2.0 ** -24 * parts)
+    assert abs(float(whole.double().sum()) - L) <= L * 1e-4   # the LSE's tolerance a row
