@@ -1040,7 +1040,7 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
   p.page_size = g.page_size;
   p.max_pages = g.max_pages;
   p.num_pages = g.num_pages;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale = (float)(scale * kMassUntruncate);
   p.timeout_ns = g_timeout_ns.load();
   if (!few) {
     const cudaError_t e = cudaMemsetAsync(workspace, 0, (size_t)g.batch * g.max_ctx * 8, stream);
