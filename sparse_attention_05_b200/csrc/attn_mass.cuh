@@ -7,29 +7,29 @@
 //
 // Per listed entry 1152 B gathered and 147456 flops: 128 flops a byte, below the ~253
 // at which this part's BF16 rate and HBM rate meet, so the gather bounds the kernel:
-// rows in HBM come at 5.2-5.9 TB/s with 112-200 KB of loads in flight per SM and 4.3 with
-// 80 KB, rows in L2 at up to 10.5 TB/s (measured, loads alone). Hence Q does not take
-// shared memory: the row's Q (128 heads x 576) is the A operand in tensor memory (288
-// columns), and shared memory is a ring of seven 28-KB stages for the listed latent rows,
-// 64 dims of up to 224 rows each. D[head][entry] = Q . K_tile^T takes the other 224
-// columns: N = 224 costs the tensor core about what N = 128 does (the operand in tensor
-// memory is read at one rate for both), so a wide tile is nearly free.
+// rows in HBM come at 5.2-6.4 TB/s with 112-200 KB of loads in flight per SM and 4.3 with
+// 80 KB, rows in L2 at up to 15 TB/s (measured, loads alone). Hence Q does not take shared
+// memory: the first 512 dims of the row's Q (128 heads x 576) are the A operand in tensor
+// memory (256 columns), only the last 64 stay in shared memory, and the rest of that is a
+// ring of six 32-KB stages for the listed latent rows, 64 dims of up to 256 rows each.
+// D[head][entry] = Q . K_tile^T takes the other 256 columns: a product with N = 256 costs
+// the tensor core little more than one with N = 128, so a wide tile is nearly free.
 //
 // One persistent CTA per SM walks (row, tile) items: with few rows an equal run of all
 // rows' tiles each (a row may be shared by several CTAs), with many every gridDim-th row
 // whole, which spreads the short rows evenly. A row's Q travels through the ring as nine
 // stages before its first tile. Tiles without a valid entry are passed over by every role.
 //
-// Warp roles (512 threads):
-//   warps 0-11  epilogue: warp w has heads 32 (w % 4) .. + 31 and the columns of third
-//               w / 4 (80, 80 and 64). It empties the accumulator into registers (there
-//               is one: the tensor core waits for no more than that), four heads of a
-//               column in a thread, takes the exponentials and sums a column in the thread
-//               and over the eight lanes that share it (with one head a lane the sums took
-//               31 exchanges for 32 columns, not 7, and 512 rows 215 us, not 199); the
-//               four partial sums of a column meet in shared memory
-//   warp 12     TMEM, and the issue of the copies of Q into it and of the products
-//   warps 13-15 producers: a warp's cp.async covers four whole 128-B lines, eight lanes a
+// Warp roles (640 threads):
+//   warps 0-15  epilogue: warp w has heads 32 (w % 4) .. + 31 and columns 64 (w / 4) .. + 63.
+//               It empties the accumulator into registers (there is one: the tensor core
+//               waits for no more than that), four heads of a column in a thread, takes the
+//               exponentials and sums a column in the thread and over the eight lanes that
+//               share it (with one head a lane the sums took 31 exchanges for 32 columns,
+//               not 7, and 512 rows 215 us, not 199); the four partial sums of a column
+//               meet in shared memory
+//   warp 16     TMEM, and the issue of the copies of Q into it and of the products
+//   warps 17-19 producers: a warp's cp.async covers four whole 128-B lines, eight lanes a
 //               line (one line a lane would take eight times the tag lookups). Entries are
 //               read two tiles ahead and their pages one tile ahead. Where the list has
 //               no entry the cache's first row is copied and its column dropped (a copy
@@ -52,17 +52,19 @@ namespace dsa {
 constexpr int kMassHeads = 128;
 constexpr int kMassDqk = 576;
 constexpr int kMassChunks = kMassDqk / 64;
-constexpr int kMassMaxTile = 224;                  // entries of a tile (MMA N), at most
-constexpr int kMassThird = 80;                     // columns of an epilogue warp, at most
-constexpr int kMassStages = 7;
+constexpr int kMassMaxTile = 256;                  // entries of a tile (MMA N), at most
+constexpr int kMassQuarter = kMassMaxTile / 4;     // columns of an epilogue warp
+constexpr int kMassStages = 6;
 constexpr int kMassStageBytes = kMassMaxTile * 128;
-constexpr int kMassEpilogue = 384, kMassProducers = 96;
+constexpr int kMassEpilogue = 512, kMassProducers = 96;
 constexpr int kMassThreads = kMassEpilogue + 32 + kMassProducers;
-constexpr int kMassQCols = kMassDqk / 2;           // tensor memory columns of Q
-constexpr int kMassSmemBytes = 1024 + kMassStages * kMassStageBytes +
+constexpr int kMassQCols = 256;                    // tensor memory columns of Q's chunks 0-7
+constexpr int kMassQBytes = kMassHeads * 128;      // its last chunk, in shared memory
+constexpr int kMassSmemBytes = 1024 + kMassStages * kMassStageBytes + kMassQBytes +
                                2 * 4 * kMassMaxTile * 4 /*partial sums*/ + 24 * 8 + 16;
 static_assert(kMassSmemBytes <= 232448, "attention mass shared memory exceeds the per-CTA limit");
 static_assert(kMassQCols + kMassMaxTile <= 512, "tensor memory");
+static_assert(kMassStages < kMassChunks, "Q's last chunk is free once its place in the ring is");
 constexpr float kMassUnit = 1099511627776.0f;             // 2^40 units of fixed point
 constexpr float kMassMaxP = 64.0f;                        // a larger p is not a weight
 // The tensor core truncates its running sums: after the 36 dependent steps of a logit it is
@@ -87,7 +89,7 @@ struct MassParams {
   int32_t k, batch, max_ctx, q_per_seq, num_q;
   int32_t row_begin, row_count;
   int32_t paged, page_size, max_pages, num_pages;
-  int32_t tile;                // entries of a tile: a multiple of 16, at most 224
+  int32_t tile;                // entries of a tile: a multiple of 16, at most 256
   int32_t ntiles;              // of a row
   int32_t whole_rows;          // CTAs take whole rows instead of runs of tiles
   float scale;
@@ -183,7 +185,7 @@ struct MassRing {
   }
 };
 
-// 16 lanes x 32 (or 16) columns of tensor memory: register 4 j + 2 r + c of a thread holds
+// 16 lanes x 32 columns of tensor memory: register 4 j + 2 r + c of a thread holds
 // lane l / 4 + 8 r, column 8 j + 2 (l % 4) + c (l: the thread's lane).
 __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -195,14 +197,6 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
 // Waits for this thread's tensor memory loads; ties the registers to the wait.
 template <int N>
 __device__ __forceinline__ void tmem_wait_ld_tie(uint32_t (&r)[N]) {
@@ -211,11 +205,10 @@ __device__ __forceinline__ void tmem_wait_ld_tie(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// A block of 8 G columns of a warp's 32 heads: this thread's logits of heads l / 4 and + 8
+// A block of 32 columns of a warp's 32 heads: this thread's logits of heads l / 4 and + 8
 // (lo), + 16 and + 24 (hi).
-template <int G>
 struct MassBlock {
-  uint32_t lo[4 * G], hi[4 * G];
+  uint32_t lo[16], hi[16];
   __device__ __forceinline__ void load(uint32_t taddr) {
     tmem_ld_16x256b(taddr, lo);
     tmem_ld_16x256b(taddr + (16u << 16), hi);
@@ -226,27 +219,23 @@ struct MassBlock {
   }
   // The weights, summed over the warp's heads: four in the thread, then halving exchanges
   // over the eight lanes that share its columns. Every column is summed in the same order.
-  // Lane l gets column 16 b4 + 8 b3 + b2 + 2 (l % 4) by its bits (G = 2: without b4's).
+  // Lane l gets column 16 b4 + 8 b3 + b2 + 2 (l % 4) by its bits.
   // The difference scale z - LSE is rounded as such: with log2 e inside both terms a weight
   // would also lose what their size costs.
   __device__ __forceinline__ float sum(float scale, const float (&lse)[4], int lane) const {
     auto weight = [&](uint32_t z, int r) {
       return ex2_approx(1.4426950408889634f * fmaf(__uint_as_float(z), scale, -lse[r]));
     };
-    float v[2 * G];
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
+    for (int j = 0; j < 4; ++j) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         v[2 * j + c] = (weight(lo[4 * j + c], 0) + weight(lo[4 * j + 2 + c], 1)) +
                        (weight(hi[4 * j + c], 2) + weight(hi[4 * j + 2 + c], 3));
     }
-    if (G == 2) {
 #pragma unroll
-      for (int i = 0; i < 2 * G; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
-    }
-#pragma unroll
-    for (int n = G, o = G == 2 ? 8 : 16; n > 0; n >>= 1, o >>= 1) {
+    for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
       const bool up = lane & o;
 #pragma unroll
       for (int i = 0; i < n; ++i) {
@@ -263,7 +252,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  float* sPart = reinterpret_cast<float*>(ring + kMassStages * kMassStageBytes);  // [2][4][224]
+  uint8_t* sQ = ring + kMassStages * kMassStageBytes;        // Q's last chunk
+  float* sPart = reinterpret_cast<float*>(sQ + kMassQBytes);  // [2][4][256]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sPart + 2 * 4 * kMassMaxTile);
   uint64_t* kfull = bars;                    // [stages] the stage's copies are complete
   uint64_t* kempty = kfull + kMassStages;    // [stages] it was read
@@ -285,7 +275,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     *abort_flag = 0;
     fence_mbarrier_init_cluster();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
@@ -297,9 +287,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   int drain_dummy = 0;
   volatile int* no_abort = &drain_dummy;
 
-  if (warp >= 13) {
+  if (warp >= 17) {
     // ------------------------------------------------------------ producers
-    const int pw = warp - 13, piece = lane & 7, sub = lane >> 3;
+    const int pw = warp - 17, piece = lane & 7, sub = lane >> 3;
     // rows of this warp: per from pw * per on, a multiple of four
     const int per = (p.tile / 4 + 2) / 3 * 4;
     constexpr int kGroups = (kMassMaxTile / 4 + 2) / 3;  // of four rows
@@ -356,7 +346,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < kMassChunks && ok; ++c) {
             if (!acquire()) break;
-            const uint32_t dst = smem_u32(ring + at.stage * kMassStageBytes);
+            // (the products that read the last chunk are done: two stages of this Q are read)
+            const uint32_t dst = smem_u32(c < kMassChunks - 1 ? ring + at.stage * kMassStageBytes
+                                                              : sQ);
 #pragma unroll
             for (int i = 0; i < 11; ++i) {
               const int h = (pw * 11 + i) * 4 + sub;
@@ -395,7 +387,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       for (int i = 0; i < 3; ++i) own0[i] = own1[i], own1[i] = own2[i], page0[i] = page1[i];
     }
     cp_async_wait_all();
-  } else if (warp == 12) {
+  } else if (warp == 16) {
     // ------------------------------------------------------------ MMA issuer
     MassRing at;
     uint32_t tiles = 0;
@@ -425,14 +417,21 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           const uint32_t src = smem_u32(ring + st.stage * kMassStageBytes);
           const int c = stages - i <= kMassChunks ? i - (stages - kMassChunks) : -1;
           if (c < 0) {  // a chunk of Q; the products that follow see it
+            if (i < kMassChunks - 1) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tmem_copy_128x32(tmem_q + i * 32 + kk * 8, smem_desc_sw128(src + kk * 32, 16, 1024));
-          } else {
+              for (int kk = 0; kk < 4; ++kk)
+                tmem_copy_128x32(tmem_q + i * 32 + kk * 8, smem_desc_sw128(src + kk * 32, 16, 1024));
+            }
+          } else if (c < kMassChunks - 1) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_bf16_ts(tmem_d, tmem_q + c * 32 + kk * 8, smem_desc_sw128(src + kk * 32, 16, 1024),
                           idesc, (c > 0 || kk > 0) ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ss(tmem_d, smem_desc_sw128(smem_u32(sQ) + kk * 32, 16, 1024),
+                          smem_desc_sw128(src + kk * 32, 16, 1024), idesc, 1u);
           }
           mma_commit(smem_u32(&kempty[st.stage]));
         }
@@ -449,7 +448,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const int quad = warp & 3, third = warp >> 2;
+    const int quad = warp & 3, quarter = warp >> 2;
     const int head = quad * 32 + (lane >> 2);  // and + 8, + 16, + 24
     const int column = (lane & 16) + (lane & 8) + ((lane >> 2) & 1) + 2 * (lane & 3);
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -481,26 +480,19 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         const bool got = warp != 0 || warp_wait(smem_u32(tfull), tiles & 1, TO, abort_flag);
         if (!named_barrier_and(1, kMassEpilogue, got)) break;
         tc_fence_after();
-        MassBlock<4> za, zb;
-        MassBlock<2> zc;
-        const uint32_t col = tmem_d + lane_off + third * kMassThird;
+        MassBlock za, zb;
+        const uint32_t col = tmem_d + lane_off + quarter * kMassQuarter;
         za.load(col);
         zb.load(col + 32);
-        if (third < 2) zc.load(col + 64);
         za.wait();
         zb.wait();
-        if (third < 2) zc.wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(tempty));
-        const int n = now.columns(p) - third * kMassThird;
-        float* part = sPart + ((tiles & 1) * 4 + quad) * kMassMaxTile + third * kMassThird;
+        const int n = now.columns(p) - quarter * kMassQuarter;
+        float* part = sPart + ((tiles & 1) * 4 + quad) * kMassMaxTile + quarter * kMassQuarter;
         if (n > 0) part[column] = za.sum(p.scale, lse, lane);
         if (n > 32) part[32 + column] = zb.sum(p.scale, lse, lane);
-        if (n > 64 && third < 2) {
-          const float v = zc.sum(p.scale, lse, lane);
-          if (lane < 16) part[64 + column] = v;
-        }
         named_barrier_sync(2, kMassEpilogue);
         if (tid < kMassMaxTile) {
           const float* all = sPart + (tiles & 1) * 4 * kMassMaxTile + tid;
@@ -528,7 +520,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem_q, 512);
   }
