@@ -34,7 +34,9 @@ def _nvcc() -> str:
 # the header that holds each kernel (for per-kernel digests)
 KERNEL_HEADER = {"indexer": "indexer.cuh", "topk": "topk.cuh", "sparse_mla": "sparse_mla.cuh",
                  "indexer_kl": "indexer_kl.cuh", "mask": "mha_prefill.cuh",
-                 "up_proj": "mha_prefill.cuh", "masked_mha": "mha_prefill.cuh"}
+                 "up_proj": "mha_prefill.cuh", "masked_mha": "mha_prefill.cuh",
+                 "rope": "rope.cuh", "cache_append": "cache.cuh", "cache_compact": "cache.cuh",
+                 "attn_mass": "attn_mass.cuh", "evict_select": "evict.cuh"}
 
 
 def source_digest(kernel=None) -> str:

@@ -65,6 +65,7 @@ def _call_rope(lib, d, x=FAKE, out=OTHER, pos=FAKE, f=FAKE):
     (dict(num_rows=-1), 1), (dict(magnitude=float("nan")), 1), (dict(magnitude=float("inf")), 1),
     (dict(x_row_stride=-1), 1), (dict(num_rows=1 << 31), 2),
     (dict(dim=1024, rot_begin=0, rot_dim=514, x_head_stride=1024, out_head_stride=1024), 2),
+    (dict(heads=65536), 2), (dict(dim=32769, x_head_stride=1 << 17, out_head_stride=1 << 17), 2),
     (dict(out_head_stride=95), 1),      # heads of the output overlap
     (dict(out_head_stride=0), 1),
     (dict(out_row_stride=383), 1),      # rows of the output overlap
@@ -138,6 +139,9 @@ def test_evict_and_compact_refusals(lib):
         assert sel(**{name: None}) == 1, name
     assert sel(ld=511) == 1 and sel(keep=0, sink=0, recent=0) == 1
     assert sel(sink=-1) == 1 and sel(recent=-1) == 1 and sel(keep=4) == 1
+    kv = _kv(batch=1, max_ctx=(1 << 22) + 1)
+    assert sel(ld=1 << 23) == 2
+    kv = _kv()
 
     def com(a=FAKE, b=FAKE, c=FAKE, mass=FAKE, ld=512, kept=FAKE, keep=8, lens=FAKE, dst=None,
             ta=None, tb=None, tc=None, tm=None, tld=0):

@@ -188,6 +188,22 @@ def test_select_against_a_sort(kind, ctx, keep, sink, recent):
     _check_select(m.contiguous(), lens, keep, sink, recent)
 
 
+@pytest.mark.parametrize("ctx", [400001, 1 << 22])
+def test_select_from_very_long_contexts(ctx):
+    """Beyond the keys that shared memory holds, up to the longest context; many ties."""
+    g = torch.Generator(device=DEV).manual_seed(ctx)
+    m = (torch.rand(2, ctx, generator=g, device=DEV) * 1000).round()
+    lens, keep, sink, recent = [ctx, ctx - 12345], 150000, 7, 1001
+    kept, new = dsa.dsa_evict_select(m, dsa.KvLayout(2, ctx, _i32(lens)), keep, sink, recent)
+    assert dsa.dsa_get_device_error() == 0 and new.tolist() == [keep, keep]
+    for b, n in enumerate(lens):
+        middle = m[b, sink:n - recent]
+        best = middle.sort(descending=True, stable=True).indices[:keep - sink - recent].sort().values
+        at = torch.arange(ctx, device=DEV)
+        want = torch.cat([at[:sink], best + sink, at[n - recent:n]])
+        assert torch.equal(kept[b].long(), want)
+
+
 def test_select_reports_a_length_out_of_range():
     m = torch.rand(3, 100, device=DEV)
     kept, new = dsa.dsa_evict_select(m, dsa.KvLayout(3, 100, _i32([101, -1, 90])), 10)
@@ -292,6 +308,37 @@ def test_compact_reports_bad_lists():
         assert dsa.dsa_get_device_error() == 5
         assert torch.equal(kv[0], before[0])
         assert torch.equal(kv[1, :4], before[1, [3, 9, 11, 13]])
+
+
+def test_caches_past_32_bits():
+    """Appending to, weighing, choosing from and moving out of the last slots of a cache whose
+    latent rows span 4.6 GB."""
+    ctx = 4_000_000
+    kv = torch.zeros(1, ctx, 576, device=DEV, dtype=torch.bfloat16)
+    codes = torch.zeros(1, ctx, 128, device=DEV, dtype=torch.uint8)
+    scale = torch.zeros(1, ctx, device=DEV)
+    lay = dsa.KvLayout(1, ctx)
+    lat = torch.randn(3, 576, device=DEV).bfloat16()
+    key = torch.randn(3, 128, device=DEV).bfloat16()
+    f, _ = dsa.rope_freqs(64, device=DEV)
+    dsa.dsa_cache_append(lat, key, kv, codes, scale, lay, 3, f, idx_interleaved=None)
+    assert torch.equal(kv[0, -3:, :512], lat[:, :512]) and torch.all(scale[0, -3:] > 0)
+    assert not kv[0, :-3].any() and not scale[0, :-3].any()
+    q = torch.randn(3, 128, 576, device=DEV).bfloat16()
+    idx = _i32([[0, ctx - 3, -1], [5, ctx - 3, ctx - 2], [7, ctx - 2, ctx - 1]])
+    out, lse = dsa.dsa_sparse_mla_fwd(q, kv, lay, 3, idx, 576 ** -0.5)
+    mass = torch.zeros(1, ctx, device=DEV)
+    dsa.dsa_attn_mass(q, kv, lay, 3, idx, 576 ** -0.5, lse, mass)
+    assert abs(float(mass.double().sum()) - 3) < 3e-4
+    assert set(mass[0].nonzero().flatten().tolist()) == {0, 5, 7, ctx - 3, ctx - 2, ctx - 1}
+    kept, new = dsa.dsa_evict_select(mass, lay, 6)
+    assert kept.tolist() == [[0, 5, 7, ctx - 3, ctx - 2, ctx - 1]]
+    last = [t[0, -3:].clone() for t in (kv, codes, scale, mass)]
+    dsa.dsa_cache_compact(kv, codes, scale, lay, kept, new, mass=mass)
+    assert dsa.dsa_get_device_error() == 0
+    for t, w in zip((kv, codes, scale, mass), last):
+        assert torch.equal(t[0, 3:6], w)
+    assert not mass[0, 6:].any() and torch.equal(kv[0, -3:], last[0])
 
 
 def test_trimming_twice_and_captured():

@@ -45,6 +45,7 @@ def _check(x, positions, freqs, m, got, angle=0.0, **kw):
 @pytest.mark.parametrize("rows,heads,before,rot,after", [
     (1, 1, 0, 64, 0), (2, 128, 512, 64, 0), (67, 3, 16, 32, 8), (300, 1, 0, 2, 0),
     (5, 7, 3, 10, 1), (33, 64, 0, 64, 64), (3, 2, 0, 512, 0), (2, 3, 1, 64, 7),
+    (3, 2, 4000, 64, 1000), (2, 2, 8, 32, 24), (1000, 16, 8, 64, 0), (2, 1, 700, 6, 301),
 ])
 def test_forward_and_backward(dtype, interleaved, rows, heads, before, rot, after):
     g = torch.Generator(device=DEV).manual_seed(rows * 131 + heads)
@@ -102,6 +103,22 @@ def test_strided_views_and_untouched_neighbours(dtype):
     with pytest.raises(dsa.DSAError):                                  # one row into the next
         dsa.dsa_rope(buf.view(-1, 128)[:-1], pos[0].expand(23).contiguous(), f,
                      buf.view(-1, 128)[1:])
+
+
+def test_many_heads_and_offsets_past_32_bits():
+    f, m = dsa.rope_freqs(2, device=DEV)
+    x = torch.randn(1, 65535, 2, device=DEV)
+    pos = torch.tensor([12345], device=DEV, dtype=torch.int32)
+    _check(x, pos, f, m, dsa.dsa_rope(x, pos, f))
+    f, m = dsa.rope_freqs(64, device=DEV)
+    buf = torch.zeros((1 << 32) + 4096, device=DEV, dtype=torch.bfloat16)  # 8 GB
+    far = buf.as_strided((3, 2, 64), (1 << 31, 128, 1))
+    far.copy_(torch.randn(3, 2, 64, device=DEV))
+    pos = torch.tensor([1, 2, 3], device=DEV, dtype=torch.int32)
+    out = torch.empty(3, 2, 64, device=DEV, dtype=torch.bfloat16)
+    _check(far, pos, f, m, dsa.dsa_rope(far, pos, f, out))
+    dsa.dsa_rope(far, pos, f, far)
+    assert torch.equal(far, out)
 
 
 def test_gradient_is_the_transpose_and_matches_differences():
