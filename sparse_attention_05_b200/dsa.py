@@ -590,15 +590,17 @@ def _device(t: torch.Tensor) -> int:
 
 def _kv_desc(kv: KvLayout, device: int, q_start: Optional[torch.Tensor] = None) -> KvDescC:
     """kv.c() with its tensors' types, sizes and device checked (and q_start's size)."""
-    if kv.seqlens is not None:
-        _need("seqlens", kv.seqlens, torch.int32, (kv.batch,), device)
-    if kv.block_table is not None:
-        if kv.block_table.dim() != 2 or kv.block_table.shape[0] != kv.batch:
-            raise ValueError("block_table must be [batch, max_pages]")
-        _need("block_table", kv.block_table, torch.int32, None, device)
+    lens, table = kv.seqlens, kv.block_table
+    if lens is not None:
+        lens = _need("seqlens", lens, torch.int32, (kv.batch,), device)
     if q_start is not None:
         _need("q_start", q_start, torch.int32, (kv.batch + 1,), device)
-    return kv.c()
+    if table is None:
+        return KvDescC(DSA_KV_CONTIGUOUS, kv.batch, kv.max_ctx, 0, 0, 0, None, lens)
+    if table.dim() != 2 or table.shape[0] != kv.batch:
+        raise ValueError("block_table must be [batch, max_pages]")
+    return KvDescC(DSA_KV_PAGED, kv.batch, kv.max_ctx, kv.page_size, kv.num_pages, table.shape[1],
+                   _need("block_table", table, torch.int32, None, device), lens)
 
 
 def _rows_shape(kv: KvLayout):
