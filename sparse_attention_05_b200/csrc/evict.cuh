@@ -16,6 +16,8 @@
 // other CTAs (the whole histograms would be 56 KB a CTA over distributed shared memory).
 #pragma once
 
+#include <type_traits>
+
 #include "ptx.cuh"
 
 namespace dsa {
@@ -193,31 +195,43 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
   uint32_t* bits_at = bits_above + (p.run >> 5);      // [run / 32]
   uint32_t* keys = bits_at + (p.run >> 5);            // [run] where they are held
   auto key_at = [&](int i) { return p.hold ? keys[i] : evict_key(__ldg(mass + i)); };
-  // adds a key to a histogram; the slots no query ever chose share one key, and a warp
-  // counts those at once
-  auto add = [&](int pass, int digit, uint32_t key, bool member) {
-    const uint32_t zeros = __ballot_sync(0xffffffffu, member && key == kEvictZero);
-    if (member && (key != kEvictZero || lane == __ffs(zeros) - 1))
-      atomicAdd(&sh.hist[pass == 0 && (lane & 1) ? 3 : pass][digit],
-                key == kEvictZero ? __popc(zeros) : 1);
-  };
   for (int i = tid; i < 4 * kEvictBins; i += kEvictThreads) (&sh.hist[0][0])[i] = 0;
   __syncthreads();
-  for (int i0 = warp * 32; i0 < count; i0 += kEvictThreads * kEvictLoads) {
+  // The slots no query ever chose share one key; a thread counts its own of them.
+  int zeros = 0;
+  auto add = [&](int* hist, int digit, uint32_t key, bool member) {
+    if (member && key == kEvictZero) ++zeros;
+    if (member && key != kEvictZero) atomicAdd(hist + digit, 1);
+  };
+  auto add_zeros = [&](int* bin) {
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if (lane == 0 && zeros) atomicAdd(bin, zeros);
+    zeros = 0;
+  };
+  int* first = sh.hist[lane & 1 ? 3 : 0];
+  auto histogram = [&](int i0, auto whole) {  // whole: all of the warp's slots are the CTA's
+    constexpr bool kWhole = decltype(whole)::value;
     float m[kEvictLoads];  // in flight at once
 #pragma unroll
     for (int j = 0; j < kEvictLoads; ++j) {
       const int i = i0 + j * kEvictThreads + lane;
-      m[j] = i < count ? __ldg(mass + i) : 0.f;
+      m[j] = kWhole || i < count ? __ldg(mass + i) : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < kEvictLoads; ++j) {
       const int i = i0 + j * kEvictThreads + lane;
       const uint32_t key = evict_key(m[j]);
-      if (p.hold && i < count) keys[i] = key;
-      add(0, key >> 21, key, i < count);
+      if (p.hold && (kWhole || i < count)) keys[i] = key;
+      add(first, key >> 21, key, kWhole || i < count);
     }
+  };
+  for (int i0 = warp * 32; i0 < count; i0 += kEvictThreads * kEvictLoads) {
+    if (i0 + kEvictThreads * (kEvictLoads - 1) + 32 <= count)
+      histogram(i0, std::true_type{});
+    else
+      histogram(i0, std::false_type{});
   }
+  add_zeros(&sh.hist[0][kEvictZero >> 21]);
   evict_digit(sh, 0, want, p.splits);
   const uint32_t top = sh.found[0];
   int left = sh.found[1];
@@ -225,20 +239,20 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
 #pragma unroll 4
   for (int i0 = warp * 32; i0 < count; i0 += kEvictThreads) {
     const bool in = i0 + lane < count;
-    const uint32_t key = in ? key_at(i0 + lane) : 0u;
-    const uint32_t above = __ballot_sync(0xffffffffu, in && (key >> 21) > top);
-    const bool at = in && (key >> 21) == top;
+    const uint32_t key = in ? key_at(i0 + lane) : 0u, digit = key >> 21;
+    const uint32_t above = __ballot_sync(0xffffffffu, in && digit > top);
+    const bool at = in && digit == top;
     const uint32_t equal = __ballot_sync(0xffffffffu, at);
     if (lane == 0) {
       bits_above[i0 >> 5] = above;
       bits_at[i0 >> 5] = equal;
     }
-    if (equal) add(1, (key >> 10) & 2047, key, at);
+    if (equal) add(sh.hist[1], (key >> 10) & 2047, key, at);
   }
+  add_zeros(&sh.hist[1][0]);
   // the slots of the second bitmap against a digit: above it, or still at it. A thread
   // takes whole words, each from another bit on (the keys then lie in different banks).
   auto refine = [&](int shift, uint32_t mask, uint32_t digit, bool next) {
-    int zeros = 0;
     for (int w = tid; w < words; w += kEvictThreads) {
       uint32_t todo = __funnelshift_r(bits_at[w], bits_at[w], lane), above = 0, at = 0;
       while (todo) {
@@ -249,14 +263,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
           above |= 1u << bit;
         } else if (d == digit) {
           at |= 1u << bit;
-          if (key == kEvictZero) ++zeros;
-          else if (next) atomicAdd(&sh.hist[2][key & 1023], 1);
+          if (next) add(sh.hist[2], key & 1023, key, true);
         }
       }
       bits_above[w] |= above;
       bits_at[w] = at;
     }
-    if (next && zeros) atomicAdd(&sh.hist[2][0], zeros);
+    if (next) add_zeros(&sh.hist[2][0]);
   };
   evict_digit(sh, 1, left, p.splits);
   const uint32_t second = sh.found[0];
