@@ -27,6 +27,11 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictGroup = kEvictBins / kEvictWarps;  // bins of one partial sum
 constexpr int kEvictLoads = 16;           // of a thread, in flight
+// Slots of a bitmap word up to which its own thread writes them: the stores of a warp's
+// threads lie apart, but there are few. Denser words are written by the whole warp, a word at
+// a time. (128 x 131072, keeping an eighth: 81 us by threads, 85 by warps; half of tied masses:
+// 240 and 133.)
+constexpr int kEvictSparse = 16;
 constexpr int kEvictMaxSplits = 8;
 constexpr int kEvictMaxKeys = 45056;      // keys a CTA holds in shared memory (176 KB)
 constexpr int kEvictMaxCtx = 1 << 22;     // two bits a slot fit in shared memory up to here
@@ -317,10 +322,20 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
       g += a, e += c;
     }
     for (int over = ne - max(0, left - be); over > 0 && at; --over) at &= ~(0x80000000u >> __clz(at));
-    // a thread writes its own word's slots: neighbours write next to each other
-    int32_t* to = kept + p.sink + bg + min(be, left);
-    for (uint32_t word = above | at; word; word &= word - 1)
-      *to++ = begin + w * 32 + __ffs(word) - 1;
+    const uint32_t word = above | at;
+    int place = p.sink + bg + min(be, left);
+    if (__reduce_max_sync(0xffffffffu, (uint32_t)__popc(word)) <= kEvictSparse) {
+      for (uint32_t todo = word; todo; todo &= todo - 1)
+        kept[place++] = begin + w * 32 + __ffs(todo) - 1;
+    } else {
+#pragma unroll 4
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t m = __shfl_sync(0xffffffffu, word, j);
+        const int to = __shfl_sync(0xffffffffu, place, j);
+        if ((m >> lane) & 1)
+          kept[to + __popc(m & ((1u << lane) - 1))] = begin + (w0 + warp * 32 + j) * 32 + lane;
+      }
+    }
     __syncthreads();
   }
   cluster_sync_all();  // no CTA leaves while another still reads its shared memory
