@@ -454,8 +454,9 @@ DSA_API dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_str
  *         (a weight above 64 or NaN, which no such lse gives, makes the slot's mass NaN);
  *         k in [1, 2^20]
  *  mass   fp32 [batch][mass_ld], mass_ld >= max_ctx, by slot; added to
- *  workspace  device, 256-byte aligned, dsa_attn_mass_workspace_size() bytes; written
- *         during the call (stream order), nothing kept in it. Many rows (for the
+ *  workspace  device, 256-byte aligned, dsa_attn_mass_workspace_size() bytes (0 for one
+ *         row a sequence: then it may be NULL); written during the call (stream order),
+ *         nothing kept in it. Many rows (for the
  *         caches' size) are summed in units of 2^-40, a few in fp32. */
 DSA_API size_t dsa_attn_mass_workspace_size(const dsa_kv_desc_t* kv, const dsa_q_desc_t* q,
                                             int32_t k);

@@ -36,8 +36,10 @@
 //               with a zero-fill operand takes 1.6 times as long to issue).
 //
 // The sums over the rows are the same for every order of execution:
+//   one row a sequence: p is added to the mass where it is computed (equal entries of one
+//     row carry equal p, so their order is free);
 //   few rows a sequence: p goes to the workspace, and one CTA a sequence adds its rows
-//     one after another (equal entries of one row carry equal p, so their order is free);
+//     one after another;
 //   many rows: p is added as a 64-bit integer in units of 2^-40, which commutes, and a
 //     second kernel turns the sums into fp32. 2^-41 is the most an entry is off.
 #pragma once
@@ -82,6 +84,7 @@ struct MassParams {
   const int32_t* block_table;
   const int32_t* seqlens;
   const int32_t* q_start;
+  // where the weights go: one of these, else to the mass itself
   float* p_out;                // [batch * row_count][k], or nullptr
   unsigned long long* sums;    // [batch][max_ctx], or nullptr
   float* mass;                 // [batch][mass_ld]
@@ -502,17 +505,18 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       }
       w *= 1.0f / kMassHeads;
       const int e = now.tile * p.tile + tid;
-      if (p.sums) {
-        if (slot >= 0) {
-          unsigned long long* s = p.sums + (int64_t)now.b * p.max_ctx + slot;
-          if (w <= kMassMaxP)
-            atomicAdd(s, (unsigned long long)__float2ll_rn(w * kMassUnit));
-          else
-            atomicOr(s, kMassNan);
-        }
-      } else if (now.t >= 0 && tid < p.tile && e < p.k) {
-        p.p_out[(int64_t)now.row * p.k + e] =
-            slot < 0 ? 0.f : w <= kMassMaxP ? w : __int_as_float(0x7fffffff);
+      const float weight = w <= kMassMaxP ? w : __int_as_float(0x7fffffff);
+      if (p.p_out) {
+        if (now.t >= 0 && tid < p.tile && e < p.k)
+          p.p_out[(int64_t)now.row * p.k + e] = slot < 0 ? 0.f : weight;
+      } else if (slot >= 0) {
+        unsigned long long* s = p.sums + (int64_t)now.b * p.max_ctx + slot;
+        if (!p.sums)
+          atomicAdd(p.mass + (int64_t)now.b * p.mass_ld + slot, weight);
+        else if (w <= kMassMaxP)
+          atomicAdd(s, (unsigned long long)__float2ll_rn(w * kMassUnit));
+        else
+          atomicOr(s, kMassNan);
       }
     }
   }

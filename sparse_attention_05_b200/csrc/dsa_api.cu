@@ -1000,6 +1000,7 @@ bool mass_few_rows(const Geometry& g, int k) {
 }
 
 size_t mass_workspace(const Geometry& g, int k) {
+  if (g.row_count == 1) return 0;
   return mass_few_rows(g, k) ? align256((size_t)g.batch * g.row_count * k * 4)
                              : align256((size_t)g.batch * g.max_ctx * 8);
 }
@@ -1022,10 +1023,10 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
   p.block_table = g.block_table;
   p.seqlens = g.seqlens;
   p.q_start = g.q_start;
-  const bool few = mass_few_rows(g, k);
+  const bool one = g.row_count == 1, few = !one && mass_few_rows(g, k);
   if (few)
     p.p_out = reinterpret_cast<float*>(workspace);
-  else
+  else if (!one)
     p.sums = reinterpret_cast<unsigned long long*>(workspace);
   p.mass = mass;
   p.mass_ld = mass_ld;
@@ -1042,7 +1043,7 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
   p.num_pages = g.num_pages;
   p.scale = (float)(scale * kMassUntruncate);
   p.timeout_ns = g_timeout_ns.load();
-  if (!few) {
+  if (p.sums) {
     const cudaError_t e = cudaMemsetAsync(workspace, 0, (size_t)g.batch * g.max_ctx * 8, stream);
     if (e != cudaSuccess) return DSA_ERR_CUDA;
   }
@@ -1063,6 +1064,7 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
   const unsigned grid = (unsigned)std::min<int64_t>(sms, p.whole_rows ? rows : tiles);
   attn_mass_kernel<<<grid, kMassThreads, kMassSmemBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+  if (one) return DSA_OK;
   if (few)
     mass_add_rows_kernel<<<(unsigned)g.batch, kMassAddThreads, 0, stream>>>(p);
   else
@@ -1599,8 +1601,9 @@ dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const dsa_kv_des
   if (!aligned16(q) || !aligned16(kv_cache) || (reinterpret_cast<uintptr_t>(mass) & 3))
     return DSA_ERR_INVALID_ARG;
   if (g.batch > 65535) return DSA_ERR_UNSUPPORTED_SHAPE;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-      workspace_bytes < mass_workspace(g, k))
+  const size_t need = mass_workspace(g, k);
+  if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+               workspace_bytes < need))
     return DSA_ERR_WORKSPACE;
   return launch_attn_mass(q, kv_cache, g, idx, k, scale, lse, mass, mass_ld, workspace,
                           (cudaStream_t)stream);

@@ -727,7 +727,8 @@ def dsa_attn_mass(q, kv_cache, kv: KvLayout, q_per_seq: int, idx, scale: float, 
                   q_start=None) -> torch.Tensor:
     """The head mean of the window's attention weights added to mass [batch, >= max_ctx], by
     slot (include/dsa.h): idx [T, k] and lse [T, 128] as the forward used and wrote them;
-    ``workspace`` is a 256-B aligned device tensor (a fresh one when None)."""
+    ``workspace`` is a 256-B aligned device tensor (a fresh one when None, none for one row a
+    sequence)."""
     T, k, dev = q.shape[0], idx.shape[1], _device(q)
     kvd, qd = _kv_desc(kv, dev, q_start), _qdesc(T, q_per_seq, rows, q_start)
     ref, qref = ctypes.byref(kvd), ctypes.byref(qd)
@@ -736,11 +737,14 @@ def dsa_attn_mass(q, kv_cache, kv: KvLayout, q_per_seq: int, idx, scale: float, 
             _need("idx", idx, torch.int32, (T, k), dev), k, scale,
             _need("lse", lse, torch.float32, (T, HEADS), dev), _mass_ptr("mass", mass, kv, dev),
             mass.shape[1])
+    nbytes = 0
     if workspace is None:
-        workspace = _new(max(256, lib().dsa_attn_mass_workspace_size(ref, qref, k)), torch.uint8,
-                         q, stream)
-    _call("dsa_attn_mass", dev, stream, *args, _ptr(workspace),
-          workspace.numel() * workspace.element_size())
+        need = lib().dsa_attn_mass_workspace_size(ref, qref, k)
+        if need:
+            workspace, nbytes = _new(need, torch.uint8, q, stream), need
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _call("dsa_attn_mass", dev, stream, *args, _ptr(workspace), nbytes)
     return mass
 
 

@@ -123,8 +123,11 @@ def test_attn_mass_refusals(lib):
     assert _mass(lib, k=0) == 2 and _mass(lib, k=(1 << 20) + 1) == 2
     assert _mass(lib, scale=0.0) == 1 and _mass(lib, scale=float("nan")) == 1
     assert _mass(lib, ld=511) == 1
-    assert _mass(lib, ws=None) == 6 and _mass(lib, ws=ctypes.c_void_p(0x100080)) == 6
-    assert _mass(lib, nb=100) == 6
+    two = dsa.QDescC(4, 2, 0, 0)    # with one row a sequence there is no workspace
+    assert _mass(lib, q=two, ws=None) == 6 and _mass(lib, q=two, ws=ctypes.c_void_p(0x100080)) == 6
+    assert _mass(lib, q=two, nb=100) == 6
+    assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(dsa.QDescC(2, 1, 0, 0)), 16) == 0
+    assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(two), 16) == 256
     assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(dsa.QDescC(2, 1, 0, 0)), 0) == 0
     assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(dsa.QDescC(3, 1, 0, 0)), 16) == 0
     assert _mass(lib, kv=_kv(batch=65536, max_ctx=16), q=dsa.QDescC(65536, 1, 0, 0), ld=16) == 2

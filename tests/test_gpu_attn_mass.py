@@ -176,10 +176,11 @@ def test_bad_page_and_bad_rows_are_reported():
 def test_own_workspace_other_stream_and_graph():
     p = synth.decode(batch=2, ctx=400, q_per_seq=1, seed=88)
     idx = _idx(p, 200, 9)
-    n = dsa.dsa_attn_mass_workspace_size(dsa.KvLayout(2, 400), 2, 1, 200)
-    _check(p, idx, workspace=torch.empty(n, dtype=torch.uint8, device=DEV))
+    two = synth.decode(batch=2, ctx=400, q_per_seq=2, seed=91)
+    n = dsa.dsa_attn_mass_workspace_size(dsa.KvLayout(2, 400), 4, 2, 200)
+    _check(two, _idx(two, 200, 12), workspace=torch.empty(n, dtype=torch.uint8, device=DEV))
     g = p.to(DEV)
-    for rows in (1, 12):
+    for rows in (1, 2, 12):
         q = g.q.repeat_interleave(rows, 0)
         li = torch.from_numpy(np.repeat(idx, rows, 0)).cuda()
         lse = torch.full((2 * rows, 128), 6.0, device=DEV)
@@ -199,9 +200,9 @@ def test_own_workspace_other_stream_and_graph():
         assert torch.equal(mass, want)
 
 
-def test_the_two_ways_of_summing_agree():
-    """One batch both ways: the window of all its rows at once (integers), and row by row (each
-    call adds a few rows in fp32): apart by at most 2^-41 and one fp32 step per entry."""
+def test_the_ways_of_summing_agree():
+    """One batch three ways: the window of all its rows at once (integers), two rows and one row
+    a call (fp32): apart by at most 2^-41 and one fp32 step per entry."""
     p = synth.ragged([300, 200], [12, 12], seed=89)
     idx = _idx(p, 100, 11)
     g = p.to(DEV)
@@ -209,15 +210,18 @@ def test_the_two_ways_of_summing_agree():
     lay = dsa.KvLayout.of(g)
     lse = torch.full((p.num_q, 128), 6.0, device=DEV)
     sizes = [dsa.dsa_attn_mass_workspace_size(lay, p.num_q, 12, 100, rows=w, q_start=g.q_start)
-             for w in (None, (0, 1))]
+             for w in (None, (0, 2), (0, 1))]
     up = lambda n: -(-n // 256) * 256  # noqa: E731
-    assert sizes == [up(2 * p.max_ctx * 8), up(2 * 100 * 4)]  # the two workspaces
-    whole, single = torch.zeros(2, p.max_ctx, device=DEV), torch.zeros(2, p.max_ctx, device=DEV)
-    dsa.dsa_attn_mass(g.q, g.kv, lay, 12, li, p.scale, lse, whole, q_start=g.q_start)
-    for i in range(12):
-        dsa.dsa_attn_mass(g.q, g.kv, lay, 12, li, p.scale, lse, single, rows=(i, 1),
-                          q_start=g.q_start)
-    assert torch.all((whole - single).abs() <= 12 * 2.0 ** -41 + 13 * 2.0 ** -24 * single)
+    assert sizes == [up(2 * p.max_ctx * 8), up(2 * 2 * 100 * 4), 0]  # the three ways
+    got = []
+    for step in (12, 2, 1):
+        mass = torch.zeros(2, p.max_ctx, device=DEV)
+        for i in range(0, 12, step):
+            dsa.dsa_attn_mass(g.q, g.kv, lay, 12, li, p.scale, lse, mass, rows=(i, step),
+                              q_start=g.q_start)
+        got.append(mass)
+    assert torch.all((got[0] - got[1]).abs() <= 12 * 2.0 ** -41 + 13 * 2.0 ** -24 * got[1])
+    assert torch.equal(got[1], got[2])      # the same additions in the same order
 
 
 def test_long_prefill_agrees_with_its_windows():
