@@ -452,7 +452,7 @@ DSA_API dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_str
  * the GPU runs the rows.
  *  q, kv_cache, idx, scale as for dsa_sparse_mla_fwd and lse as it wrote it for them
  *         (a weight above 64 or NaN, which no such lse gives, makes the slot's mass NaN);
- *         k in [1, 2^20]
+ *         k in [1, 2^20], batch <= 65535
  *  mass   fp32 [batch][mass_ld], mass_ld >= max_ctx, by slot; added to
  *  workspace  device, 256-byte aligned, dsa_attn_mass_workspace_size() bytes (0 for one
  *         row a sequence: then it may be NULL); written during the call (stream order),

@@ -1541,6 +1541,7 @@ dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_stride, con
     return DSA_ERR_INVALID_ARG;
   if (!(std::fabs(magnitude) < 1e30f)) return DSA_ERR_INVALID_ARG;
   if (g.num_q == 0) return DSA_OK;
+  if ((int64_t)g.batch * g.row_count >= (1ll << 31)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!latent_new || !k_new) return DSA_ERR_INVALID_ARG;
   if (!aligned16(latent_new) || !aligned16(k_new) || !aligned16(kv_cache) || !aligned16(k_idx) ||
       (reinterpret_cast<uintptr_t>(k_scale) & 3) || (reinterpret_cast<uintptr_t>(freqs) & 7) ||
@@ -1600,7 +1601,8 @@ dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const dsa_kv_des
   if (!q || !idx || !lse) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv_cache) || (reinterpret_cast<uintptr_t>(mass) & 3))
     return DSA_ERR_INVALID_ARG;
-  if (g.batch > 65535) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (g.batch > 65535 || (int64_t)g.batch * g.row_count >= (1ll << 31))
+    return DSA_ERR_UNSUPPORTED_SHAPE;
   const size_t need = mass_workspace(g, k);
   if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
                workspace_bytes < need))

@@ -107,6 +107,9 @@ def test_append_refusals(lib):
     assert _append(lib, m=float("nan")) == 1
     assert _append(lib, q=dsa.QDescC(3, 1, 0, 0)) == 1
     assert _append(lib, kv=_kv(layout=1, page=48, pages=4, max_pages=16, bt=0x2000)) == 2
+    # more window rows (batch * q_per_seq) than a grid takes
+    many = _kv(batch=1 << 16, max_ctx=1 << 16, layout=1, page=64, pages=1024, max_pages=1024, bt=0x2000)
+    assert _append(lib, kv=many, q=dsa.QDescC(5, 1 << 16, 0, 0, 0x3000)) == 2
     # a ragged batch without a single new token
     assert _append(lib, q=dsa.QDescC(0, 1, 0, 0, 0x3000), lat=None, key=None) == 0
 
@@ -130,6 +133,8 @@ def test_attn_mass_refusals(lib):
     assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(two), 16) == 256
     assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(dsa.QDescC(2, 1, 0, 0)), 0) == 0
     assert lib.dsa_attn_mass_workspace_size(by(_kv()), by(dsa.QDescC(3, 1, 0, 0)), 16) == 0
+    many = _kv(batch=65535, max_ctx=1 << 16, layout=1, page=64, pages=1024, max_pages=1024, bt=0x2000)
+    assert _mass(lib, kv=many, q=dsa.QDescC(5, 1 << 16, 0, 0, 0x3000), ld=1 << 16) == 2
     assert _mass(lib, kv=_kv(batch=65536, max_ctx=16), q=dsa.QDescC(65536, 1, 0, 0), ld=16) == 2
 
 
