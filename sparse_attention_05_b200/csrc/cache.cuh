@@ -115,8 +115,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
 // order, and plain CTAs take them.
 constexpr int kCompactThreads = 256;
 constexpr int kCompactSlices = 11;
-constexpr int kCompactRows = kCompactThreads;            // rows of a CTA's chunk
-constexpr int kCompactSmemBytes = 2 * kCompactRows * 128;
+// A CTA's chunk: 256 or 512 rows (one or two entries of a lane), two of them in shared memory.
+constexpr int kCompactRows = kCompactThreads;
+constexpr int compact_smem_bytes(int entries) { return 2 * entries * kCompactRows * 128; }
 
 struct CompactParams {
   const uint8_t* kv;
@@ -147,7 +148,7 @@ __device__ __forceinline__ int cache_row(const int32_t* table, int b, int slot, 
   return pg * page_size + slot % page_size;
 }
 
-template <bool kInPlace>
+template <bool kInPlace, int kEntries>
 __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const CompactParams p) {
   extern __shared__ uint4 compact_smem[];
   const int b = blockIdx.x / p.splits, rank = blockIdx.x % p.splits;
@@ -159,9 +160,11 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
     return;
   }
   const int32_t* kept = p.kept + (int64_t)b * p.keep;
-  const int step = p.splits * kCompactRows;
-  // this lane's entry of chunk c, whose row its warp moves
-  auto entry = [&](int c) { return c * step + rank * kCompactRows + tid; };
+  const int step = p.splits * kEntries * kCompactRows;
+  // this lane's e-th entry of chunk c, whose row its warp moves
+  auto entry = [&](int c, int e) {
+    return c * step + (rank * kEntries + e) * kCompactRows + tid;
+  };
   // its source row; -1: none, or already in its place
   auto source = [&](int i, int& slot) {
     if (i >= n) return -1;
@@ -191,56 +194,78 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
     const int64_t pitch = slice < 9 ? 1152 : 128;
     const uint8_t* from = (slice < 9 ? p.kv + slice * 128 : p.k_idx) + piece * 16;
     uint8_t* to = (slice < 9 ? p.to_kv + slice * 128 : p.to_k_idx) + piece * 16;
-    uint4* mine = compact_smem + (warp * 32 + sub) * 8 + piece;  // + buffer, + 32 a group of rows
-    auto load = [&](int c) {
-      int slot;
-      const int row = c < chunks ? source(entry(c), slot) : -1;
+    // a lane's pieces in shared memory: + 32 a group of four rows, + kCompactRows * 8 an entry
+    uint4* mine = compact_smem + (warp * 32 + sub) * 8 + piece;
+    auto buffer = [&](int c) { return mine + (c & 1) * kEntries * kCompactRows * 8; };
+    auto load = [&](int c, int (&row)[kEntries]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = __shfl_sync(0xffffffffu, row, j * 4 + sub);
-        if (r >= 0)
-          cp_async_16(smem_u32(mine + (c & 1) * kCompactRows * 8 + j * 32), from + r * pitch, 16u);
+      for (int e = 0; e < kEntries; ++e) {
+        int slot;
+        row[e] = c < chunks ? source(entry(c, e), slot) : -1;
+      }
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = __shfl_sync(0xffffffffu, row[e], j * 4 + sub);
+          if (r >= 0)
+            cp_async_16(smem_u32(buffer(c) + e * kCompactRows * 8 + j * 32), from + r * pitch, 16u);
+        }
       }
       cp_async_commit();
-      return row;
     };
-    int row = load(0);
+    int row[kEntries], next[kEntries], dst[kEntries];
+    load(0, row);
     for (int c = 0; c < chunks; ++c) {
-      const int next = load(c + 1);
-      const int dst = row >= 0 ? destination(entry(c)) : -1;
+      load(c + 1, next);
+#pragma unroll
+      for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
       cp_async_wait_group<1>();
       all_loaded();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = __shfl_sync(0xffffffffu, dst, j * 4 + sub);
-        if (r >= 0)
-          *reinterpret_cast<uint4*>(to + r * pitch) = mine[(c & 1) * kCompactRows * 8 + j * 32];
+      for (int e = 0; e < kEntries; ++e) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = __shfl_sync(0xffffffffu, dst[e], j * 4 + sub);
+          if (r >= 0)
+            *reinterpret_cast<uint4*>(to + r * pitch) = buffer(c)[e * kCompactRows * 8 + j * 32];
+        }
+        row[e] = next[e];
       }
-      row = next;
     }
     return;
   }
-  float s = 0.f, m = 0.f;
-  auto load = [&](int c) {
-    int slot;
-    const int row = c < chunks ? source(entry(c), slot) : -1;
-    if (row >= 0) {
-      s = p.k_scale[row];
-      if (p.mass) m = p.mass[(int64_t)b * p.mass_ld + slot];
+  float s[kEntries], m[kEntries];
+  auto load = [&](int c, int (&row)[kEntries]) {
+#pragma unroll
+    for (int e = 0; e < kEntries; ++e) {
+      int slot;
+      row[e] = c < chunks ? source(entry(c, e), slot) : -1;
+      if (row[e] >= 0) {
+        s[e] = p.k_scale[row[e]];
+        if (p.mass) m[e] = p.mass[(int64_t)b * p.mass_ld + slot];
+      }
     }
-    return row;
   };
-  int row = load(0);
+  int row[kEntries], next[kEntries];
+  load(0, row);
   for (int c = 0; c < chunks; ++c) {
-    const float s0 = s, m0 = m;
-    const int next = load(c + 1);
-    const int dst = row >= 0 ? destination(entry(c)) : -1;
+    float s0[kEntries], m0[kEntries];
+    int dst[kEntries];
+#pragma unroll
+    for (int e = 0; e < kEntries; ++e) s0[e] = s[e], m0[e] = m[e];
+    load(c + 1, next);
+#pragma unroll
+    for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
     all_loaded();
-    if (dst >= 0) {
-      p.to_k_scale[dst] = s0;
-      if (p.mass) p.to_mass[(int64_t)b * p.to_mass_ld + entry(c)] = m0;
+#pragma unroll
+    for (int e = 0; e < kEntries; ++e) {
+      if (dst[e] >= 0) {
+        p.to_k_scale[dst[e]] = s0[e];
+        if (p.mass) p.to_mass[(int64_t)b * p.to_mass_ld + entry(c, e)] = m0[e];
+      }
+      row[e] = next[e];
     }
-    row = next;
   }
   if (p.mass)
     for (int i = n + rank * kCompactThreads + tid; i < min(len, p.to_max_ctx);

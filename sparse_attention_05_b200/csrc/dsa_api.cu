@@ -956,37 +956,42 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
 // CTAs per slice. Into other pages about twelve for every SM (three are resident): 48
 // sequences of 8192 kept tokens took 195 us with three for every SM, 185 with twelve. In
 // place they form a cluster (of at most eight, the portable size), which moves its chunks
-// in order, and six for every SM are enough (168 us; 172 with twelve).
-dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStream_t stream) {
+// in order, and six for every SM are enough (168 us; 172 with twelve); where the clusters
+// leave SMs idle they take chunks of twice the rows, half as many steps.
+template <bool kInPlace, int kEntries>
+dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t attr_err = once_per_device(once, [] {
-    const cudaError_t e = cudaFuncSetAttribute(
-        cache_compact_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmemBytes);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(cache_compact_kernel<true>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       kCompactSmemBytes);
+    return cudaFuncSetAttribute(cache_compact_kernel<kInPlace, kEntries>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                compact_smem_bytes(kEntries));
   });
   if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
-  const int64_t chunks = (p.keep + kCompactRows - 1) / kCompactRows;
-  const int64_t fill = ((in_place ? 6 : 12) * num_sms() + (int64_t)batch * kCompactSlices - 1) /
-                       ((int64_t)batch * kCompactSlices);
-  p.splits = (int)std::min(chunks, fill);
-  if (in_place)
-    p.splits = p.splits >= 8 ? 8 : p.splits >= 4 ? 4 : p.splits >= 2 ? 2 : 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)batch * p.splits), kCompactSlices, 1);
   cfg.blockDim = dim3(kCompactThreads, 1, 1);
-  cfg.dynamicSmemBytes = kCompactSmemBytes;
+  cfg.dynamicSmemBytes = compact_smem_bytes(kEntries);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = in_place ? p.splits : 1;
+  attr[0].val.clusterDim.x = kInPlace ? p.splits : 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(in_place ? cudaLaunchKernelEx(&cfg, cache_compact_kernel<true>, p)
-                              : cudaLaunchKernelEx(&cfg, cache_compact_kernel<false>, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, cache_compact_kernel<kInPlace, kEntries>, p));
+}
+
+dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStream_t stream) {
+  const int64_t chunks = (p.keep + kCompactRows - 1) / kCompactRows;
+  const int64_t fill = ((in_place ? 6 : 12) * num_sms() + (int64_t)batch * kCompactSlices - 1) /
+                       ((int64_t)batch * kCompactSlices);
+  p.splits = (int)std::min(chunks, fill);
+  if (!in_place) return launch_compact_kernel<false, 1>(p, batch, stream);
+  p.splits = p.splits >= 8 ? 8 : p.splits >= 4 ? 4 : p.splits >= 2 ? 2 : 1;
+  return (int64_t)batch * kCompactSlices * p.splits <= num_sms()
+             ? launch_compact_kernel<true, 2>(p, batch, stream)
+             : launch_compact_kernel<true, 1>(p, batch, stream);
 }
 
 // ---- attention mass ----------------------------------------------------------------
