@@ -473,7 +473,7 @@ DSA_API dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const ds
  *  kv        batch, max_ctx (at most 2^22) and seqlens are used
  *  keep      >= 1 and >= sink + recent
  *  kept      int32 [batch][keep] out: the slots that stay, ascending, padded with -1
- *  new_lens  int32 [batch] out: min(seqlen, keep). */
+ *  new_lens  int32 [batch] out: min(seqlen, keep); not kv's seqlens array itself. */
 DSA_API dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_desc_t* kv,
                                       int32_t keep, int32_t sink, int32_t recent, int32_t* kept,
                                       int32_t* new_lens, dsa_stream_t stream);
@@ -490,7 +490,8 @@ DSA_API dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const 
  *  dst       NULL: in place (the dst pointers must be NULL, dst_mass_ld is ignored).
  *            Otherwise the geometry of the destination (batch as kv's, seqlens ignored),
  *            whose cache arrays may be the source's own as long as no destination slot
- *            is a slot of any source sequence (pages fresh from the pool).
+ *            is a slot of any source sequence (pages fresh from the pool; both paged).
+ *  dst_mass  fp32 [batch][dst_mass_ld], apart from mass; NULL where mass is
  * No two sequences may share the slots they are trimmed in. */
 DSA_API dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, float* mass,
                                        int64_t mass_ld, const dsa_kv_desc_t* kv,

@@ -1626,6 +1626,7 @@ dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_d
   if (!mass || !kept || !new_lens || mass_ld < g.max_ctx) return DSA_ERR_INVALID_ARG;
   if (keep < 1 || sink < 0 || recent < 0 || sink > keep || recent > keep - sink)
     return DSA_ERR_INVALID_ARG;
+  if (new_lens == kv->seqlens) return DSA_ERR_INVALID_ARG;  // read while it is written
   if ((reinterpret_cast<uintptr_t>(mass) & 3) || (reinterpret_cast<uintptr_t>(kept) & 3) ||
       (reinterpret_cast<uintptr_t>(new_lens) & 3))
     return DSA_ERR_INVALID_ARG;
@@ -1654,6 +1655,12 @@ dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, floa
     st = check_geometry(dst, &qd, &t);
     if (st != DSA_OK) return st;
     if (!dst_kv_cache || !dst_k_idx || !dst_k_scale || !mass != !dst_mass)
+      return DSA_ERR_INVALID_ARG;
+    // the chunks move in no order: the same slots would be read after they are written
+    if (dst_kv_cache == kv_cache && (!g.block_table || !t.block_table || g.block_table == t.block_table))
+      return DSA_ERR_INVALID_ARG;
+    if (mass && mass < dst_mass + (int64_t)t.batch * dst_mass_ld &&
+        dst_mass < mass + (int64_t)g.batch * mass_ld)
       return DSA_ERR_INVALID_ARG;
   }
   if (mass && (mass_ld < g.max_ctx || dst_mass_ld < t.max_ctx)) return DSA_ERR_INVALID_ARG;

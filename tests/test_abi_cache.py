@@ -147,6 +147,8 @@ def test_evict_and_compact_refusals(lib):
         assert sel(**{name: None}) == 1, name
     assert sel(ld=511) == 1 and sel(keep=0, sink=0, recent=0) == 1
     assert sel(sink=-1) == 1 and sel(recent=-1) == 1 and sel(keep=4) == 1
+    kv.seqlens = FAKE.value
+    assert sel() == 1                             # new_lens over the lengths it reads
     kv = _kv(batch=1, max_ctx=(1 << 22) + 1)
     assert sel(ld=1 << 23) == 2
     kv = _kv()
@@ -164,6 +166,12 @@ def test_evict_and_compact_refusals(lib):
     assert com(**dict(to, tm=None)) == 1          # mass without a place for it
     assert com(**dict(to, tld=63)) == 1
     assert com(**dict(to, dst=_kv(batch=3, max_ctx=64))) == 1
+    assert com(**dict(to, ta=FAKE)) == 1          # contiguous into itself
+    assert com(**dict(to, tm=ctypes.c_void_p(FAKE.value + 512 * 4))) == 1   # mass into its second row
+    kv = _kv(layout=1, page=64, pages=64, max_pages=8, bt=0x2000)
+    same = _kv(max_ctx=64, layout=1, page=64, pages=64, max_pages=8, bt=0x2000)
+    assert com(**dict(to, dst=same, ta=FAKE)) == 1  # the same pages
+    kv = _kv()
     assert com(**dict(to, dst=_kv(layout=1, page=32, pages=4, max_pages=16, bt=0x2000))) == 2
 
 
