@@ -1016,8 +1016,12 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
                               cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t attr_err = once_per_device(once, [] {
-    return cudaFuncSetAttribute(attn_mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kMassSmemBytes);
+    const cudaError_t e = cudaFuncSetAttribute(
+        attn_mass_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMassSmemBytes);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(attn_mass_kernel<true>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kMassSmemBytes);
   });
   if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
   MassParams p{};
@@ -1067,7 +1071,10 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
   // turn are as even and spread the short ones (and load each Q once)
   p.whole_rows = rows >= 16ll * sms;
   const unsigned grid = (unsigned)std::min<int64_t>(sms, p.whole_rows ? rows : tiles);
-  attn_mass_kernel<<<grid, kMassThreads, kMassSmemBytes, stream>>>(p);
+  if (p.tile == kMassMaxTile && k % kMassMaxTile == 0)
+    attn_mass_kernel<true><<<grid, kMassThreads, kMassSmemBytes, stream>>>(p);
+  else
+    attn_mass_kernel<false><<<grid, kMassThreads, kMassSmemBytes, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (one) return DSA_OK;
   if (few)

@@ -88,7 +88,7 @@ def _idx(p, k, seed):
     return _lists(p.num_q, oracle_args(p)["q_pos"], k, seed)
 
 
-@pytest.mark.parametrize("k", [1, 100, 128, 129, 225, 700, 2000])
+@pytest.mark.parametrize("k", [1, 100, 128, 129, 225, 512, 700, 2000])
 def test_decode(k):
     p = synth.decode(batch=3, ctx=900, q_per_seq=1, seed=70 + k)
     mass0, mass = _check(p, _idx(p, k, k))
@@ -128,9 +128,11 @@ def test_listed_as_it_comes():
     _check(p, idx)
 
 
-def test_prefill_rows_shorter_than_the_list():
-    p = synth.prefill(L=200, seed=85)
-    _check(p, _idx(p, 128, 6))
+@pytest.mark.parametrize("L,k", [(200, 128), (330, 256)])
+def test_prefill_rows_shorter_than_the_list(L, k):
+    """The second: as many entries as the widest tile, every tile full but for the padding."""
+    p = synth.prefill(L=L, seed=85)
+    _check(p, _idx(p, k, 6))
 
 
 def test_nan_only_where_it_is_listed():
@@ -224,11 +226,12 @@ def test_the_ways_of_summing_agree():
     assert torch.equal(got[1], got[2])      # the same additions in the same order
 
 
-def test_long_prefill_agrees_with_its_windows():
+@pytest.mark.parametrize("k", [300, 512])
+def test_long_prefill_agrees_with_its_windows(k):
     """So many rows that a CTA takes whole ones in turn, some of them with tiles without an
     entry, against windows of a hundred rows (runs of tiles): integer sums of the same weights,
     added to fp32 once and 25 times."""
-    L, k = 2500, 300
+    L = 2500
     g = torch.Generator(device=DEV).manual_seed(90)
     q = (torch.randn(L, 128, 576, device=DEV, generator=g) * 2).bfloat16()
     kv = (torch.randn(1, L, 576, device=DEV, generator=g) * 0.5).bfloat16()
