@@ -431,12 +431,13 @@ DSA_API dsa_status_t dsa_rope_bwd(const void* dout, const int32_t* positions, co
  *                codes E4M3(k / s) to nearest even; the scale cache gets s. A key with a
  *                NaN gets NaN codes and a NaN scale.
  * All other cache rows stay as they were.
- *  latent_new  bf16 [T] rows of 576, latent_stride elements apart (a multiple of 8)
- *  k_new       bf16 [T] rows of 128, k_stride elements apart (a multiple of 8)
+ *  latent_new  bf16 [T] rows of 576, latent_stride elements apart (a multiple of 8, at most 2^30)
+ *  k_new       bf16 [T] rows of 128, k_stride elements apart (a multiple of 8, at most 2^30)
  *  positions   int32 [T] rotary positions, or NULL for the slots
  *  freqs       fp64 [32], magnitude as in dsa_rope
  *  kv_cache, k_idx, k_scale  the caches, as dsa_sparse_mla_fwd and dsa_indexer_scores
- *              read them; no two rows of the window may share a slot. */
+ *              read them, apart from the new rows; no two rows of the window may share a
+ *              slot. */
 DSA_API dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_stride,
                                       const void* k_new, int64_t k_stride,
                                       const int32_t* positions, const double* freqs,

@@ -33,6 +33,10 @@ constexpr int kDIdx = 128, kMaxK = 2048;
 std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
 
 dsa_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
@@ -1561,6 +1565,12 @@ dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_stride, con
     return DSA_ERR_INVALID_ARG;
   if (latent_stride < 576 || latent_stride % 8 || k_stride < 128 || k_stride % 8)
     return DSA_ERR_INVALID_ARG;
+  // a row written might be another's, not yet read
+  if (latent_stride > (1ll << 30) || k_stride > (1ll << 30) ||
+      overlap(latent_new, ((int64_t)(g.num_q - 1) * latent_stride + 576) * 2, kv_cache,
+              g.cache_rows * 1152) ||
+      overlap(k_new, ((int64_t)(g.num_q - 1) * k_stride + 128) * 2, k_idx, g.cache_rows * 128))
+    return DSA_ERR_INVALID_ARG;
   AppendParams p{};
   p.latent = reinterpret_cast<const __nv_bfloat16*>(latent_new);
   p.keys = reinterpret_cast<const __nv_bfloat16*>(k_new);
@@ -1664,7 +1674,10 @@ dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, floa
     if (!dst_kv_cache || !dst_k_idx || !dst_k_scale || !mass != !dst_mass)
       return DSA_ERR_INVALID_ARG;
     // the chunks move in no order: the same slots would be read after they are written
-    if (dst_kv_cache == kv_cache && (!g.block_table || !t.block_table || g.block_table == t.block_table))
+    const bool own_pages = g.block_table && t.block_table && g.block_table != t.block_table;
+    if (!own_pages && (overlap(kv_cache, g.cache_rows * 1152, dst_kv_cache, t.cache_rows * 1152) ||
+                       overlap(k_idx, g.cache_rows * 128, dst_k_idx, t.cache_rows * 128) ||
+                       overlap(k_scale, g.cache_rows * 4, dst_k_scale, t.cache_rows * 4)))
       return DSA_ERR_INVALID_ARG;
     if (mass && mass < dst_mass + (int64_t)t.batch * dst_mass_ld &&
         dst_mass < mass + (int64_t)g.batch * mass_ld)

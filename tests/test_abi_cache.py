@@ -89,7 +89,7 @@ def test_rope_refuses_null_unaligned_and_overlapping(lib):
     assert _call_rope(lib, _rope(num_rows=0), x=None, out=None, pos=None, f=None) == 0
 
 
-def _append(lib, kv=None, q=None, lat=FAKE, ls=576, key=FAKE, ks=128, pos=None, f=FAKE, m=1.0,
+def _append(lib, kv=None, q=None, lat=OTHER, ls=576, key=OTHER, ks=128, pos=None, f=FAKE, m=1.0,
             ll=1, kl=0, kvc=FAKE, ki=FAKE, sc=FAKE):
     return lib.dsa_cache_append(lat, ls, key, ks, pos, f, m, ll, kl, by(kv or _kv()),
                                 by(q or dsa.QDescC(2, 1, 0, 0)), kvc, ki, sc, None)
@@ -103,6 +103,12 @@ def test_append_refusals(lib):
     assert _append(lib, sc=ctypes.c_void_p(0x100002)) == 1
     assert _append(lib, ls=568) == 1 and _append(lib, ls=580) == 1
     assert _append(lib, ks=120) == 1 and _append(lib, ks=129) == 1
+    assert _append(lib, ls=(1 << 30) + 8) == 1 and _append(lib, ks=(1 << 30) + 8) == 1
+    # new rows inside the caches: 1024 rows of 1152 and of 128 bytes
+    assert _append(lib, lat=FAKE) == 1 and _append(lib, key=FAKE) == 1
+    assert _append(lib, lat=ctypes.c_void_p(FAKE.value + 1023 * 1152)) == 1
+    assert _append(lib, key=ctypes.c_void_p(FAKE.value + 1023 * 128)) == 1
+    assert _append(lib, lat=ctypes.c_void_p(FAKE.value - 1152 - 16)) == 1   # its second row
     assert _append(lib, ll=2) == 1 and _append(lib, kl=3) == 1
     assert _append(lib, m=float("nan")) == 1
     assert _append(lib, q=dsa.QDescC(3, 1, 0, 0)) == 1
@@ -167,6 +173,10 @@ def test_evict_and_compact_refusals(lib):
     assert com(**dict(to, tld=63)) == 1
     assert com(**dict(to, dst=_kv(batch=3, max_ctx=64))) == 1
     assert com(**dict(to, ta=FAKE)) == 1          # contiguous into itself
+    assert com(**dict(to, tb=FAKE)) == 1 and com(**dict(to, tc=FAKE)) == 1
+    assert com(**dict(to, ta=ctypes.c_void_p(FAKE.value + 1023 * 1152))) == 1
+    assert com(**dict(to, tb=ctypes.c_void_p(FAKE.value - 127 * 128))) == 1
+    assert com(**dict(to, tc=ctypes.c_void_p(FAKE.value + 1023 * 4))) == 1
     assert com(**dict(to, tm=ctypes.c_void_p(FAKE.value + 512 * 4))) == 1   # mass into its second row
     kv = _kv(layout=1, page=64, pages=64, max_pages=8, bt=0x2000)
     same = _kv(max_ctx=64, layout=1, page=64, pages=64, max_pages=8, bt=0x2000)
