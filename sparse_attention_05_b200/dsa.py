@@ -743,6 +743,8 @@ def dsa_attn_mass(q, kv_cache, kv: KvLayout, q_per_seq: int, idx, scale: float, 
         if need:
             workspace, nbytes = _new(need, torch.uint8, q, stream), need
     else:
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on cuda:{dev}")
         nbytes = workspace.numel() * workspace.element_size()
     _call("dsa_attn_mass", dev, stream, *args, _ptr(workspace), nbytes)
     return mass

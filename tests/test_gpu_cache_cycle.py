@@ -115,3 +115,50 @@ def test_decode_with_trimming():
                 trims += n_before[b] > keep
     assert trims >= 6                       # every trim had something to trim
     assert int(seen[0]) == 170 and max(position[0]) == 169
+
+
+def test_two_streams_at_once():
+    """The masses of two caches and their trims, each on a stream of its own at the same time,
+    against the same calls one after another: bit for bit."""
+    batch, ctx, k, keep = 3, 4096, 1024, 1500
+    g = torch.Generator(device=DEV).manual_seed(11)
+    sets = []
+    for i in range(2):
+        lens = torch.tensor([ctx, 3000 + i, 2000], dtype=torch.int32, device=DEV)
+        n = 2                                  # rows a sequence: through the workspace
+        q = torch.randn(batch * n, 128, 576, generator=g, device=DEV).bfloat16()
+        kvc = (torch.randn(batch, ctx, 576, generator=g, device=DEV) * 0.5).bfloat16()
+        idx = torch.stack([torch.randperm(1900, generator=g, device=DEV)[:k]
+                           for _ in range(batch * n)]).int()
+        lse = torch.full((batch * n, 128), 8.0, device=DEV)
+        codes = torch.randint(0, 127, (batch, ctx, 128), generator=g, device=DEV).to(torch.uint8)
+        sc = torch.rand(batch, ctx, generator=g, device=DEV)
+        sets.append((dsa.KvLayout(batch, ctx, lens), n, q, kvc, idx, lse, codes, sc))
+    streams = [torch.cuda.Stream() for _ in sets]
+
+    def run(concurrent):
+        out = []
+        state = [(s[3].clone(), s[6].clone(), s[7].clone(), torch.zeros(batch, ctx, device=DEV))
+                 for s in sets]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, st, (kvc, codes, sc, mass) in zip(sets, streams, state):
+                with torch.cuda.stream(st):
+                    lay, n, q, _, idx, lse, _, _ = s
+                    dsa.dsa_attn_mass(q, kvc, lay, n, idx, 0.04, lse, mass)
+                    kept, new = dsa.dsa_evict_select(mass, lay, keep, sink=4, recent=100)
+                    to = dsa.KvLayout(batch, keep)
+                    dst = (torch.zeros(batch, keep, 576, device=DEV, dtype=torch.bfloat16),
+                           torch.zeros(batch, keep, 128, device=DEV, dtype=torch.uint8),
+                           torch.zeros(batch, keep, device=DEV))
+                    dm = torch.zeros(batch, keep, device=DEV)
+                    dsa.dsa_cache_compact(kvc, codes, sc, lay, kept, new, mass, to, *dst, dm)
+                    out += [kept, new, *dst, dm]
+                if not concurrent:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert dsa.dsa_get_device_error() == 0
+        return out + [m for *_, m in state]
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
