@@ -929,22 +929,34 @@ dsa_status_t launch_rope(const void* x, const int32_t* positions, const double* 
 }
 
 // ---- eviction ----------------------------------------------------------------------
-// CTAs of a sequence: one for every 4096 slots, at most the portable cluster size.
+// CTAs of a sequence: one for every 4096 slots, at most the portable cluster size, as long as
+// all run at once, two an SM (128 x 32768: two CTAs 25 us, eight in four waves 54). The keys
+// stay in shared memory where that leaves as many CTAs on an SM as there are; reading them
+// again costs less than a second wave (128 x 131072: two CTAs that read again 60 us, four
+// that hold them 85, eight 78). More CTAs in any case where two runs' bitmaps would not fit.
 dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t attr_err = once_per_device(once, [] {
-    return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kEvictMaxDynamic);
+    const cudaError_t e =
+        cudaFuncSetAttribute(evict_select_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxDynamic);
+    return e != cudaSuccess
+               ? e
+               : cudaFuncSetAttribute(evict_select_kernel<true>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxDynamic);
   });
   if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
   p.splits = 1;
-  while (p.splits < kEvictMaxSplits && (int64_t)p.splits * 4096 < p.max_ctx) p.splits *= 2;
+  while (p.splits < kEvictMaxSplits && (int64_t)p.splits * 4096 < p.max_ctx &&
+         ((int64_t)batch * p.splits <= num_sms() || p.max_ctx > p.splits * kEvictRunBits))
+    p.splits *= 2;
   p.run = (int)(((int64_t)p.max_ctx / p.splits + 32 + 31) & ~31ll);
-  p.hold = p.run <= kEvictMaxKeys;
+  const bool hold =
+      p.run <= ((int64_t)batch * p.splits <= num_sms() ? kEvictMaxKeys : kEvictPairKeys);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)batch * p.splits), 1, 1);
   cfg.blockDim = dim3(kEvictThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)p.run / 4 + (p.hold ? (size_t)p.run * 4 : 0);
+  cfg.dynamicSmemBytes = (size_t)p.run / 4 + (hold ? (size_t)p.run * 4 : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -953,7 +965,8 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, evict_select_kernel, p));
+  return cuda_status(hold ? cudaLaunchKernelEx(&cfg, evict_select_kernel<true>, p)
+                          : cudaLaunchKernelEx(&cfg, evict_select_kernel<false>, p));
 }
 
 // ---- compact -----------------------------------------------------------------------
@@ -1648,8 +1661,7 @@ dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_d
       (reinterpret_cast<uintptr_t>(new_lens) & 3))
     return DSA_ERR_INVALID_ARG;
   if (g.max_ctx > kEvictMaxCtx) return DSA_ERR_UNSUPPORTED_SHAPE;
-  EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent,
-                1, 0, 0};
+  EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent, 1, 0};
   return launch_evict(p, g.batch, (cudaStream_t)stream);
 }
 

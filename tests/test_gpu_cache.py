@@ -204,6 +204,39 @@ def test_select_from_very_long_contexts(ctx):
         assert torch.equal(kept[b].long(), want)
 
 
+@pytest.mark.parametrize("batch,ctx,keep", [(150, 30001, 9000), (300, 8200, 1000), (80, 100000, 30001),
+                                            (150, 600001, 200000)])
+@pytest.mark.parametrize("kind", ["spread", "zeros", "ties"])
+def test_select_in_large_batches(batch, ctx, keep, kind):
+    """More sequences than SMs: few CTAs each, whose keys shared memory does not always hold;
+    borders among zeros of both signs (and of the tiniest numbers) and among equal masses."""
+    g = torch.Generator(device=DEV).manual_seed(batch + ctx)
+    m = torch.rand(batch, ctx, generator=g, device=DEV)
+    if kind == "zeros":   # more is kept than is not zero; every other sequence also has denormals
+        small = torch.where(m < 0.6, torch.tensor(-0.0, device=DEV), torch.tensor(0.0, device=DEV))
+        small[::2] = torch.where(m[::2] < 0.3, torch.tensor(1e-45, device=DEV), small[::2])
+        m = torch.where(m > 0.95, m, small)
+    elif kind == "ties":
+        m = torch.ones_like(m)
+    sink, recent = 5, 70
+    lens = torch.randint(ctx // 2, ctx + 1, (batch,), generator=g, device=DEV).int()
+    lens[0], lens[1] = ctx, keep
+    kept, new = dsa.dsa_evict_select(m, dsa.KvLayout(batch, ctx, lens), keep, sink, recent)
+    assert dsa.dsa_get_device_error() == 0
+    assert torch.equal(new, lens.clamp(max=keep))
+    for b in [0, 1, 2, 3, batch // 2, batch - 2, batch - 1]:
+        n = int(lens[b])
+        at = torch.arange(n, device=DEV)
+        want = at
+        if n > keep:
+            middle = m[b, sink:n - recent]
+            order = middle.sort(descending=True, stable=True).indices   # -0 equals +0
+            best = order[:keep - sink - recent].sort().values
+            want = torch.cat([at[:sink], best + sink, at[n - recent:]])
+        assert torch.equal(kept[b, :len(want)].long(), want), f"sequence {b}"
+        assert torch.all(kept[b, len(want):] == -1)
+
+
 def test_select_reports_a_length_out_of_range():
     m = torch.rand(3, 100, device=DEV)
     kept, new = dsa.dsa_evict_select(m, dsa.KvLayout(3, 100, _i32([101, -1, 90])), 10)
