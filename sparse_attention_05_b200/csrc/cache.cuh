@@ -111,11 +111,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
 // through its chunks in order: it loads a chunk into shared memory, waits at the cluster's
 // barrier until all its CTAs have theirs, and stores it; the next chunk's loads are issued
 // before that wait. The slices are independent of each other: nine of 128 B of the latent
-// row, one of the key row, one of scale and mass. Into other pages the chunks need no
-// order, and plain CTAs take them.
+// row, one of the key row, one of scale and mass.
+// Into other pages the rows need no order: a warp takes up to 16 of them whole, four at a time
+// (1280 B of latent and key in 16-byte pieces, ten of a lane in flight): 48 sequences of 8192
+// kept tokens take 159 us, and 185 in slices, which touch every row's DRAM page nine times.
 constexpr int kCompactThreads = 256;
 constexpr int kCompactSlices = 11;
-// A CTA's chunk: 256 or 512 rows (one or two entries of a lane), two of them in shared memory.
+// A CTA's chunk in place: 256 or 512 rows (one or two entries of a lane), two of them in shared memory.
 constexpr int kCompactRows = kCompactThreads;
 constexpr int compact_smem_bytes(int entries) { return 2 * entries * kCompactRows * 128; }
 
@@ -134,7 +136,8 @@ struct CompactParams {
   const int32_t* table;        // paged source
   const int32_t* to_table;     // paged destination
   int64_t mass_ld, to_mass_ld;
-  int32_t keep, splits;        // splits: CTAs (the cluster's, in place) of one slice
+  int32_t keep, splits;        // splits: CTAs of one slice (the cluster's), or of a sequence
+  int32_t steps;               // into other pages: steps of a warp
   int32_t max_ctx, page_size, max_pages, num_pages;
   int32_t to_max_ctx, to_page_size, to_max_pages, to_num_pages;
 };
@@ -148,17 +151,79 @@ __device__ __forceinline__ int cache_row(const int32_t* table, int b, int slot, 
   return pg * page_size + slot % page_size;
 }
 
-template <bool kInPlace, int kEntries>
+// Sequence b's old and new length; false (reported) where they are out of range.
+__device__ __forceinline__ bool compact_lengths(const CompactParams& p, int b, int& len, int& n) {
+  len = p.seqlens ? __ldg(p.seqlens + b) : p.max_ctx;
+  n = __ldg(p.new_lens + b);
+  const bool ok = len >= 0 && len <= p.max_ctx && n >= 0 && n <= p.keep && n <= len &&
+                  n <= p.to_max_ctx;
+  if (!ok && threadIdx.x == 0) report_error(kErrBounds);
+  return ok;
+}
+
+constexpr int kMoveWarps = kCompactThreads / 32;
+constexpr int kMoveRows = 4;      // of a warp at a time
+constexpr int kMoveSteps = 4;     // such steps of a warp, at most
+static_assert(kMoveRows * kMoveSteps <= 32, "a lane for every row");
+__global__ void __launch_bounds__(kCompactThreads, 3) cache_move_kernel(const CompactParams p) {
+  const int b = blockIdx.x / p.splits, rank = blockIdx.x % p.splits;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int len, n;
+  if (!compact_lengths(p, b, len, n)) return;
+  const int rows = p.steps * kMoveRows;  // of this warp: a lane has the places of one
+  const int64_t i = ((int64_t)rank * kMoveWarps + warp) * rows + lane;
+  int slot = 0, from = -1, to = -1;
+  if (lane < rows && i < n) {
+    slot = __ldg(p.kept + (int64_t)b * p.keep + i);
+    if (slot >= 0 && slot < len)
+      from = cache_row(p.table, b, slot, p.max_ctx, p.page_size, p.max_pages, p.num_pages);
+    to = cache_row(p.to_table, b, (int)i, p.to_max_ctx, p.to_page_size, p.to_max_pages, p.to_num_pages);
+    if (from < 0 || to < 0) {
+      report_error(kErrBounds);
+      from = to = -1;
+    }
+  }
+  if (__any_sync(0xffffffffu, from >= 0)) {
+    constexpr int kPieces = 1280 / 16, kEach = kMoveRows * kPieces / 32;
+    // this lane's j-th piece of the rows from r0 on, nullptr where there is none
+    auto piece = [&](auto* latent, auto* keys, int row_of, int r0, int j) {
+      const int c = j * 32 + lane, r = c / kPieces, at = (c - r * kPieces) * 16;
+      const int64_t row = __shfl_sync(0xffffffffu, row_of, r0 + r);
+      auto* to = at < 1152 ? latent + row * 1152 + at : keys + row * 128 + (at - 1152);
+      return row < 0 ? nullptr : to;
+    };
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kMoveRows) {
+      uint4 v[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const uint8_t* src = piece(p.kv, p.k_idx, from, r0, j);
+        if (src) v[j] = *reinterpret_cast<const uint4*>(src);
+      }
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        uint8_t* dst = piece(p.to_kv, p.to_k_idx, to, r0, j);
+        if (dst) *reinterpret_cast<uint4*>(dst) = v[j];
+      }
+    }
+    if (from >= 0) {
+      p.to_k_scale[to] = p.k_scale[from];
+      if (p.mass) p.to_mass[(int64_t)b * p.to_mass_ld + i] = p.mass[(int64_t)b * p.mass_ld + slot];
+    }
+  }
+  if (p.mass)
+    for (int64_t z = n + (int64_t)rank * kCompactThreads + threadIdx.x; z < min(len, p.to_max_ctx);
+         z += (int64_t)p.splits * kCompactThreads)
+      p.to_mass[(int64_t)b * p.to_mass_ld + z] = 0.f;
+}
+
+template <int kEntries>
 __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const CompactParams p) {
   extern __shared__ uint4 compact_smem[];
   const int b = blockIdx.x / p.splits, rank = blockIdx.x % p.splits;
   const int slice = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int len = p.seqlens ? __ldg(p.seqlens + b) : p.max_ctx;
-  const int n = __ldg(p.new_lens + b);
-  if (len < 0 || len > p.max_ctx || n < 0 || n > p.keep || n > len || n > p.to_max_ctx) {
-    if (tid == 0) report_error(kErrBounds);
-    return;
-  }
+  int len, n;
+  if (!compact_lengths(p, b, len, n)) return;
   const int32_t* kept = p.kept + (int64_t)b * p.keep;
   const int step = p.splits * kEntries * kCompactRows;
   // this lane's e-th entry of chunk c, whose row its warp moves
@@ -169,11 +234,8 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
   auto source = [&](int i, int& slot) {
     if (i >= n) return -1;
     slot = __ldg(kept + i);
-    bool ok = slot >= 0 && slot < len;
-    if (kInPlace) {
-      ok = ok && slot >= i && (i == 0 || slot > __ldg(kept + i - 1));
-      if (ok && slot == i) return -1;
-    }
+    const bool ok = slot >= i && slot < len && (i == 0 || slot > __ldg(kept + i - 1));
+    if (ok && slot == i) return -1;
     const int row = ok ? cache_row(p.table, b, slot, p.max_ctx, p.page_size, p.max_pages,
                                    p.num_pages) : -1;
     if (row < 0) report_error(kErrBounds);
@@ -184,9 +246,6 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
                               p.to_num_pages);
     if (row < 0) report_error(kErrBounds);
     return row;
-  };
-  auto all_loaded = [&] {
-    if (kInPlace) cluster_sync_all();
   };
   const int chunks = (n + step - 1) / step;
   if (slice < 10) {  // 128 B a row; a warp instruction moves four rows, eight lanes a row
@@ -221,7 +280,7 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
       cp_async_wait_group<1>();
-      all_loaded();
+      cluster_sync_all();  // all have loaded chunk c
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) {
 #pragma unroll
@@ -257,7 +316,7 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
     load(c + 1, next);
 #pragma unroll
     for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
-    all_loaded();
+    cluster_sync_all();
 #pragma unroll
     for (int e = 0; e < kEntries; ++e) {
       if (dst[e] >= 0) {

@@ -970,16 +970,15 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
 }
 
 // ---- compact -----------------------------------------------------------------------
-// CTAs per slice. Into other pages about twelve for every SM (three are resident): 48
-// sequences of 8192 kept tokens took 195 us with three for every SM, 185 with twelve. In
-// place they form a cluster (of at most eight, the portable size), which moves its chunks
-// in order, and six for every SM are enough (168 us; 172 with twelve); where the clusters
-// leave SMs idle they take chunks of twice the rows, half as many steps.
-template <bool kInPlace, int kEntries>
+// In place: CTAs per slice, which form a cluster (of at most eight, the portable size) and move
+// its chunks in order; six for every SM (168 us for 48 sequences of 8192 kept tokens; 172 with
+// twelve). Where the clusters leave SMs idle they take chunks of twice the rows, half as many
+// steps.
+template <int kEntries>
 dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t attr_err = once_per_device(once, [] {
-    return cudaFuncSetAttribute(cache_compact_kernel<kInPlace, kEntries>,
+    return cudaFuncSetAttribute(cache_compact_kernel<kEntries>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 compact_smem_bytes(kEntries));
   });
@@ -991,24 +990,33 @@ dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kInPlace ? p.splits : 1;
+  attr[0].val.clusterDim.x = p.splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, cache_compact_kernel<kInPlace, kEntries>, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, cache_compact_kernel<kEntries>, p));
 }
 
 dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStream_t stream) {
+  if (!in_place) {
+    // fewer steps of a warp where there are few rows (one sequence of 16384: two, not four, 13
+    // us, not 15)
+    const int64_t groups = (int64_t)batch * ((p.keep + kMoveRows - 1ll) / kMoveRows);
+    p.steps = (int)std::max<int64_t>(1, std::min<int64_t>(kMoveSteps, groups / (12 * num_sms())));
+    p.splits = (p.keep - 1) / (kMoveWarps * kMoveRows * p.steps) + 1;
+    if ((int64_t)batch * p.splits >= (1ll << 31)) return DSA_ERR_UNSUPPORTED_SHAPE;
+    cache_move_kernel<<<(unsigned)((int64_t)batch * p.splits), kCompactThreads, 0, stream>>>(p);
+    return cuda_status(cudaGetLastError());
+  }
   const int64_t chunks = (p.keep + kCompactRows - 1) / kCompactRows;
-  const int64_t fill = ((in_place ? 6 : 12) * num_sms() + (int64_t)batch * kCompactSlices - 1) /
+  const int64_t fill = (6 * num_sms() + (int64_t)batch * kCompactSlices - 1) /
                        ((int64_t)batch * kCompactSlices);
   p.splits = (int)std::min(chunks, fill);
-  if (!in_place) return launch_compact_kernel<false, 1>(p, batch, stream);
   p.splits = p.splits >= 8 ? 8 : p.splits >= 4 ? 4 : p.splits >= 2 ? 2 : 1;
   return (int64_t)batch * kCompactSlices * p.splits <= num_sms()
-             ? launch_compact_kernel<true, 2>(p, batch, stream)
-             : launch_compact_kernel<true, 1>(p, batch, stream);
+             ? launch_compact_kernel<2>(p, batch, stream)
+             : launch_compact_kernel<1>(p, batch, stream);
 }
 
 // ---- attention mass ----------------------------------------------------------------
