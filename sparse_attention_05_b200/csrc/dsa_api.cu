@@ -971,9 +971,9 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
 
 // ---- compact -----------------------------------------------------------------------
 // In place: CTAs per slice, which form a cluster (of at most eight, the portable size) and move
-// its chunks in order; up to four for every SM (three are resident; 8 sequences of 16384 kept
-// tokens: clusters of four 75 us, of eight 81). Where the clusters leave SMs idle they take
-// chunks of twice the rows, half as many steps.
+// its chunks in order; six for every SM (three are resident; 48 sequences of 8192 kept tokens:
+// clusters of two 152 us, of one 156, of eight 168). Where the clusters leave SMs idle they
+// take chunks of twice the rows, half as many steps.
 template <int kEntries>
 dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream_t stream) {
   static DeviceOnce once;
@@ -1010,7 +1010,8 @@ dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStre
     return cuda_status(cudaGetLastError());
   }
   const int64_t chunks = (p.keep + kCompactRows - 1) / kCompactRows;
-  const int64_t fill = 4 * num_sms() / ((int64_t)batch * kCompactSlices);
+  const int64_t fill = (6 * num_sms() + (int64_t)batch * kCompactSlices - 1) /
+                       ((int64_t)batch * kCompactSlices);
   p.splits = (int)std::min(chunks, fill);
   p.splits = p.splits >= 8 ? 8 : p.splits >= 4 ? 4 : p.splits >= 2 ? 2 : 1;
   return (int64_t)batch * kCompactSlices * p.splits <= num_sms()
