@@ -23,7 +23,7 @@
 
 namespace dsa {
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
 
 struct AppendParams {
   const __nv_bfloat16* latent;  // [T] rows of 576, stride latent_stride

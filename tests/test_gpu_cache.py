@@ -206,10 +206,11 @@ def test_select_from_very_long_contexts(ctx):
 
 @pytest.mark.parametrize("batch,ctx,keep", [(150, 30001, 9000), (300, 8200, 1000), (80, 100000, 30001),
                                             (150, 600001, 200000)])
-@pytest.mark.parametrize("kind", ["spread", "zeros", "ties"])
+@pytest.mark.parametrize("kind", ["spread", "zeros", "ties", "infinities", "nan", "negative"])
 def test_select_in_large_batches(batch, ctx, keep, kind):
     """More sequences than SMs: few CTAs each, whose keys shared memory does not always hold;
-    borders among zeros of both signs (and of the tiniest numbers) and among equal masses."""
+    borders among zeros of both signs (and of the tiniest numbers), among equal masses, among
+    infinities of either sign and among NaN."""
     g = torch.Generator(device=DEV).manual_seed(batch + ctx)
     m = torch.rand(batch, ctx, generator=g, device=DEV)
     if kind == "zeros":   # more is kept than is not zero; every other sequence also has denormals
@@ -218,6 +219,15 @@ def test_select_in_large_batches(batch, ctx, keep, kind):
         m = torch.where(m > 0.95, m, small)
     elif kind == "ties":
         m = torch.ones_like(m)
+    elif kind == "infinities":   # the border among the lower ones, or the upper ones
+        inf = float("inf")
+        m = torch.where(m < 0.7, torch.tensor(-inf, device=DEV), m - 2)
+        m[::2] = -m[::2]
+    elif kind == "nan":
+        m = torch.where(m < 0.8, torch.tensor(float("nan"), device=DEV),
+                        torch.where(m < 0.85, torch.tensor(-float("inf"), device=DEV), m - 0.9))
+    elif kind == "negative":
+        m = -torch.exp(m * 100 - 50)
     sink, recent = 5, 70
     lens = torch.randint(ctx // 2, ctx + 1, (batch,), generator=g, device=DEV).int()
     lens[0], lens[1] = ctx, keep
@@ -229,7 +239,8 @@ def test_select_in_large_batches(batch, ctx, keep, kind):
         at = torch.arange(n, device=DEV)
         want = at
         if n > keep:
-            middle = m[b, sink:n - recent]
+            middle = m[b, sink:n - recent].double()       # NaN below -inf, here both finite
+            middle = middle.clamp(min=-1e300).nan_to_num(nan=-1e301, posinf=1e300)
             order = middle.sort(descending=True, stable=True).indices   # -0 equals +0
             best = order[:keep - sink - recent].sort().values
             want = torch.cat([at[:sink], best + sink, at[n - recent:]])
