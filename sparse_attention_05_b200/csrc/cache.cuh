@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
 // row, one of the key row, one of scale and mass.
 // Into other pages the rows need no order: a warp takes up to 16 of them whole, four at a time
 // (1280 B of latent and key in 16-byte pieces, ten of a lane in flight): 48 sequences of 8192
-// kept tokens take 159 us, and 185 in slices, which touch every row's DRAM page nine times.
+// kept tokens take 156 us, and 186 in slices, which touch every row's DRAM page nine times.
 constexpr int kCompactThreads = 256;
 constexpr int kCompactSlices = 11;
 // A CTA's chunk in place: 256 or 512 rows (one or two entries of a lane), two of them in shared memory.
