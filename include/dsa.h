@@ -409,9 +409,10 @@ typedef struct {
 
 /* Rotary positions on a part of every head (the rope part of MLA, report Appendix A):
  * pair i of row t turns by the angle positions[t] * freqs[i],
- *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos),
- * in fp32 from an angle reduced in fp64, rounded once to the output type. The other
- * dims are copied. Scaled schedules for long contexts are a matter of freqs.
+ *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos).
+ * magnitude cos and magnitude sin come from fp64, rounded to fp32 once; the products and
+ * their sum are rounded to fp32 each (nothing is contracted), the result to the output type.
+ * The other dims are copied. Scaled schedules for long contexts are a matter of freqs.
  *  positions  int32 [num_rows], any sign
  *  freqs      fp64 [rot_dim / 2]: radians per position
  *  out        as x: the same rows (in place; the dims outside the rotated part are then

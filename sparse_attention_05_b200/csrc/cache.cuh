@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
   // the lane's pair of each rotated part, and its two plain key dims
   const int l0 = p.latent_interleaved ? 2 * lane : lane, l1 = p.latent_interleaved ? l0 + 1 : lane + 32;
   const int k0 = p.key_interleaved ? 2 * lane : lane, k1 = p.key_interleaved ? k0 + 1 : lane + 32;
-  float la = __bfloat162float(lat[512 + l0]), lb = __bfloat162float(lat[512 + l1]);
+  const float la = __bfloat162float(lat[512 + l0]), lb = __bfloat162float(lat[512 + l1]);
   float ka = __bfloat162float(key[k0]), kb = __bfloat162float(key[k1]);
   const float2 kc = __bfloat1622float2(
       *reinterpret_cast<const __nv_bfloat162*>(key + 64 + 2 * lane));
@@ -83,12 +83,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
   dst[lane] = n0;
   dst[32 + lane] = n1;
   __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(dst) + 512;
-  rope[l0] = __float2bfloat16_rn(la * cs.x - lb * cs.y);
-  rope[l1] = __float2bfloat16_rn(la * cs.y + lb * cs.x);
+  const float2 l = rope_pair(la, lb, cs);
+  rope[l0] = __float2bfloat16_rn(l.x);
+  rope[l1] = __float2bfloat16_rn(l.y);
   if (p.key_rotated) {
-    const float a = ka * cs.x - kb * cs.y;
-    kb = ka * cs.y + kb * cs.x;
-    ka = a;
+    const float2 k = rope_pair(ka, kb, cs);
+    ka = k.x, kb = k.y;
   }
   // the largest magnitude by its bits: a NaN anywhere makes the scale a NaN
   auto bits = [](float v) { return __float_as_uint(v) & 0x7fffffffu; };

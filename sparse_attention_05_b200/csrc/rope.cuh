@@ -7,14 +7,14 @@
 // query's dims to it (DeepSeek-V3.2-Exp technical report, Appendix A: the rope part).
 //
 // The kernel moves 2 x (row bytes) and computes three flops a dim, so memory bounds it.
-// The angle is formed in fp64 turns and reduced to [-1/2, 1/2] before it becomes fp32:
-// at position 10^6 an fp32 product would be off by 0.06 rad. A thread owns one unit (a run
-// of dims with their partners, or as many dims to copy) of one row and takes it through
-// several heads with its sines and cosines in registers; the block forms each of them once,
-// in shared memory, while the first loads are on their way. What is left is bytes in
-// flight: five blocks an SM whose threads have two runs of 16 B under way each carry 8192
-// rows of 64 bf16 heads (half of 128 dims rotated) in 55 us, four blocks with four runs in
-// 63, three in 67.
+// The angle, its sine and its cosine are formed in fp64: at position 10^6 an fp32 product
+// would be off by 0.06 rad. A thread owns one unit (a run of dims with their partners, or as
+// many dims to copy) of one row and takes it through several heads with its sines and cosines
+// in registers; the block forms each of them once, in shared memory, while the first loads
+// are on their way. What is left is bytes in flight: five blocks an SM whose threads have two
+// runs of 16 B under way each carry 8192 rows of 64 bf16 heads (half of 128 dims rotated) in
+// 51 us (55 with runs unpacked as they arrived; then four blocks with four runs took 63, three
+// 67).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -46,13 +46,34 @@ struct RopeParams {
   float magnitude, sign;     // sign = -1: transposed
 };
 
-// cos and sin of pos * freq, times magnitude.
+// cos and sin of pos * freq, times magnitude, in fp64 and rounded to fp32 once. Less than an
+// eighth of a turn is left after the quarters (q); the Taylor series to x^13 and x^14 are
+// within 2^-45 there. (65536 appended tokens take 39 us with them, 41 with the library's pair.)
 __device__ __forceinline__ float2 rope_turn(int32_t pos, double freq, float magnitude) {
   double turns = (double)pos * (freq * 0.15915494309189533577);
-  turns -= rint(turns);
-  float s, c;
-  sincospif(2.0f * (float)turns, &s, &c);
-  return make_float2(c * magnitude, s * magnitude);
+  turns = 4.0 * (turns - rint(turns));
+  const double q = rint(turns);
+  const double x = (turns - q) * 1.57079632679489661923, y = -x * x;
+  double s = 1.0 / 6227020800.0, c = 1.0 / 87178291200.0;
+  s = fma(s, y, 1.0 / 39916800.0), c = fma(c, y, 1.0 / 479001600.0);
+  s = fma(s, y, 1.0 / 362880.0), c = fma(c, y, 1.0 / 3628800.0);
+  s = fma(s, y, 1.0 / 5040.0), c = fma(c, y, 1.0 / 40320.0);
+  s = fma(s, y, 1.0 / 120.0), c = fma(c, y, 1.0 / 720.0);
+  s = fma(s, y, 1.0 / 6.0), c = fma(c, y, 1.0 / 24.0);
+  s = fma(s, y, 1.0), c = fma(c, y, 0.5);
+  s *= x, c = fma(c, y, 1.0);
+  const int quarter = (int)q & 3;
+  const float fs = (float)((quarter & 1 ? c : s) * magnitude);
+  const float fc = (float)((quarter & 1 ? s : c) * magnitude);
+  return make_float2(quarter == 1 || quarter == 2 ? -fc : fc, quarter >= 2 ? -fs : fs);
+}
+
+// A pair turned: the products and their sum are rounded to fp32 one by one, not contracted, so
+// that a rotated value has the same bits wherever it is formed (an appended key's scale and
+// codes hang on the last bit of its largest value).
+__device__ __forceinline__ float2 rope_pair(float a, float b, float2 cs) {
+  return make_float2(__fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y)),
+                     __fadd_rn(__fmul_rn(a, cs.y), __fmul_rn(b, cs.x)));
 }
 
 template <typename T> __device__ __forceinline__ float rope_to_float(T v);
@@ -91,14 +112,27 @@ struct RopeUnit {
     *reinterpret_cast<RopeVec<T, V>*>(out) = lo;
     if (kTwo && two) *reinterpret_cast<RopeVec<T, V>*>(out + gap) = hi;
   }
+  // The runs as they were loaded: 16-bit elements are not unpacked before this point, where
+  // they would take twice the registers.
+  __device__ __forceinline__ void packed() {
+    if constexpr (sizeof(lo) == 16) {
+      auto tie = [](RopeVec<T, V>& v) {
+        uint4 w = *reinterpret_cast<uint4*>(&v);
+        asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w));
+        v = *reinterpret_cast<RopeVec<T, V>*>(&w);
+      };
+      tie(lo);
+      if (kTwo) tie(hi);
+    }
+  }
   __device__ __forceinline__ void turn(const float2 (&t)[kPairs]) {
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
       T& first = kTwo ? lo.v[j] : lo.v[(2 * j) % V];
       T& second = kTwo ? hi.v[j] : lo.v[(2 * j + 1) % V];
-      const float a = rope_to_float(first), b = rope_to_float(second);
-      first = rope_from_float<T>(a * t[j].x - b * t[j].y);
-      second = rope_from_float<T>(a * t[j].y + b * t[j].x);
+      const float2 r = rope_pair(rope_to_float(first), rope_to_float(second), t[j]);
+      first = rope_from_float<T>(r.x);
+      second = rope_from_float<T>(r.y);
     }
   }
 };
@@ -159,6 +193,8 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const RopeParams 
   }
   __syncthreads();
   if (!active) return;
+#pragma unroll
+  for (int j = 0; j < kHeads; ++j) e[j].packed();
   float2 t[kPairs];
   if (turned) {
 #pragma unroll

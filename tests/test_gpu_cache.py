@@ -149,6 +149,54 @@ def test_append_reports_bad_pages_and_rows():
     assert dsa.dsa_get_device_error() == 5
 
 
+def test_append_bits_of_the_documented_rounding():
+    """Sine and cosine times the magnitude from fp64 rounded once, the products and their sum
+    rounded to fp32 each, then scale and codes by IEEE divisions: the same in numpy gives the same
+    bits. (At positions below 256 an fp64 angle is off by at most 2^-45; that moves one of the
+    131072 sines and cosines across a rounding border, 2^-24 apart at the most frequent, with a
+    probability of 1/16 in all.)"""
+    T, m = 2048, 1.25
+    g = torch.Generator(device=DEV).manual_seed(21)
+    lat = torch.randn(T, 576, generator=g, device=DEV).bfloat16()
+    key = torch.randn(T, 128, generator=g, device=DEV).bfloat16()
+    pos = torch.randint(0, 256, (T,), generator=g, device=DEV, dtype=torch.int32)
+    f, _ = dsa.rope_freqs(64, device=DEV)
+    kv, codes, scale, _, layout = _caches(1, T, False)
+    dsa.dsa_cache_append(lat, key, kv, codes, scale, layout(None), T, f, pos, magnitude=m)
+    angle = pos.cpu().numpy().astype(np.float64)[:, None] * f.cpu().numpy()
+    c, s = (np.cos(angle) * m).astype(np.float32), (np.sin(angle) * m).astype(np.float32)
+    ln, kn = lat.float().cpu().numpy(), key.float().cpu().numpy()
+    a, b = ln[:, 512::2], ln[:, 513::2]
+    ln[:, 512::2], ln[:, 513::2] = a * c - b * s, a * s + b * c
+    assert torch.equal(kv[0].cpu(), torch.from_numpy(ln).bfloat16())
+    a, b = kn[:, :32].copy(), kn[:, 32:64].copy()
+    kn[:, :32], kn[:, 32:64] = a * c - b * s, a * s + b * c
+    want = np.abs(kn).max(1) / np.float32(448)
+    assert np.array_equal(scale[0].cpu().numpy(), want)
+    assert np.array_equal(codes[0].cpu().numpy(), key_codes(kn, want[:, None]))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_writes_what_rope_gives(interleaved):
+    """A token's rope dims are dsa_rope's, and its key's scale and codes those of dsa_rope's fp32
+    result, bit for bit, wherever it lies."""
+    T = 3000
+    g = torch.Generator(device=DEV).manual_seed(22)
+    lat = torch.randn(T, 576, generator=g, device=DEV).bfloat16()
+    key = (torch.randn(T, 128, generator=g, device=DEV) * 5).bfloat16()
+    pos = torch.randint(-1000, 1 << 20, (T,), generator=g, device=DEV, dtype=torch.int32)
+    f, m = dsa.rope_freqs(64, scaling="yarn", factor=16.0, device=DEV)
+    kv, codes, scale, _, layout = _caches(1, T, False)
+    dsa.dsa_cache_append(lat, key, kv, codes, scale, layout(None), T, f, pos, magnitude=m,
+                         interleaved=interleaved, idx_interleaved=interleaved)
+    want = dsa.dsa_rope(lat, pos, f, rot_begin=512, interleaved=interleaved, magnitude=m)
+    assert torch.equal(kv[0], want)
+    k = dsa.dsa_rope(key.float(), pos, f, interleaved=interleaved, magnitude=m).cpu().numpy()
+    s = np.abs(k).max(1) / np.float32(448)
+    assert np.array_equal(scale[0].cpu().numpy(), s)
+    assert np.array_equal(codes[0].cpu().numpy(), key_codes(k, s[:, None]))
+
+
 # ---- selection -----------------------------------------------------------------------
 
 
