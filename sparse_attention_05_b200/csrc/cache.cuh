@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
 // (1280 B of latent and key in 16-byte pieces, ten of a lane in flight): 48 sequences of 8192
 // kept tokens take 156 us, and 186 in slices, which touch every row's DRAM page nine times.
 constexpr int kCompactThreads = 256;
+constexpr int kCompactBlock = kCompactThreads + 32;  // in place: and a warp for the barriers
 constexpr int kCompactSlices = 11;
 // A CTA's chunk in place: 256 or 512 rows (one or two entries of a lane), two of them in shared memory.
 constexpr int kCompactRows = kCompactThreads;
@@ -217,19 +218,28 @@ __global__ void __launch_bounds__(kCompactThreads, 3) cache_move_kernel(const Co
       p.to_mass[(int64_t)b * p.to_mass_ld + z] = 0.f;
 }
 
-// The cluster's barrier without a release, once this thread's copies have arrived: nothing
-// that it stored needs an order with what the others do next (no later chunk reads it), and
-// a release would wait for those stores (48 sequences 171 us, not 152).
-__device__ __forceinline__ void cluster_sync_loaded() {
-  asm volatile(
-      "barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+// All CTAs of the cluster have their chunk: this thread's copies have arrived. What has to be
+// ordered is one CTA's loads before another's stores to the same slots, which takes a release
+// and an acquire. The release waits for the releasing threads' own stores, so the last warp,
+// which moves nothing, gives it for its CTA, whose other warps have met it at the block's
+// barrier (8 sequences of 16384 kept tokens 68 us, and 80 with a release by every warp). A
+// cluster of one CTA needs the block's barrier alone.
+__device__ __forceinline__ void cluster_loaded(bool mover, int splits) {
+  __syncthreads();
+  if (splits == 1) return;
+  if (mover)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  else
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int kEntries>
-__global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const CompactParams p) {
   extern __shared__ uint4 compact_smem[];
   const int b = blockIdx.x / p.splits, rank = blockIdx.x % p.splits;
   const int slice = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool mover = tid < kCompactThreads;
   int len, n;
   if (!compact_lengths(p, b, len, n)) return;
   const int32_t* kept = p.kept + (int64_t)b * p.keep;
@@ -238,9 +248,9 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
   auto entry = [&](int c, int e) {
     return c * step + (rank * kEntries + e) * kCompactRows + tid;
   };
-  // its source row; -1: none, or already in its place
+  // its source row; -1: none, already in its place, or the warp that moves nothing
   auto source = [&](int i, int& slot) {
-    if (i >= n) return -1;
+    if (i >= n || !mover) return -1;
     slot = __ldg(kept + i);
     const bool ok = slot >= i && slot < len && (i == 0 || slot > __ldg(kept + i - 1));
     if (ok && slot == i) return -1;
@@ -288,7 +298,7 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
       cp_async_wait_group<1>();
-      cluster_sync_loaded();  // all have loaded chunk c
+      cluster_loaded(mover, p.splits);  // all have loaded chunk c
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) {
 #pragma unroll
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
 #pragma unroll
     for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
     cp_async_wait_group<1>();
-    cluster_sync_loaded();
+    cluster_loaded(mover, p.splits);
 #pragma unroll
     for (int e = 0; e < kEntries; ++e) {
       if (dst[e] >= 0) {
@@ -337,7 +347,7 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const Co
       row[e] = next[e];
     }
   }
-  if (p.mass)
+  if (p.mass && mover)
     for (int i = n + rank * kCompactThreads + tid; i < min(len, p.to_max_ctx);
          i += p.splits * kCompactThreads)
       p.to_mass[(int64_t)b * p.to_mass_ld + i] = 0.f;

@@ -971,9 +971,11 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
 
 // ---- compact -----------------------------------------------------------------------
 // In place: CTAs per slice, which form a cluster (of at most eight, the portable size) and move
-// its chunks in order; six for every SM (three are resident; 48 sequences of 8192 kept tokens:
-// clusters of two 152 us, of one 156, of eight 168). Where the clusters leave SMs idle they
-// take chunks of twice the rows, half as many steps.
+// its chunks in order; four for every SM (8 sequences of 16384 kept tokens: clusters of four 68
+// us, of eight 74; 20 of 8192: of two 82, of four 96). Two slices an SM and more go without
+// clusters, whose barrier costs more than it gives then (32 sequences of 8192 kept tokens: one
+// CTA a slice 113 us, two 125; 48: 146 and 166). Where the clusters leave SMs idle they take
+// chunks of twice the rows, half as many steps.
 template <int kEntries>
 dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream_t stream) {
   static DeviceOnce once;
@@ -985,7 +987,7 @@ dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream
   if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)batch * p.splits), kCompactSlices, 1);
-  cfg.blockDim = dim3(kCompactThreads, 1, 1);
+  cfg.blockDim = dim3(kCompactBlock, 1, 1);
   cfg.dynamicSmemBytes = compact_smem_bytes(kEntries);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1010,11 +1012,11 @@ dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStre
     return cuda_status(cudaGetLastError());
   }
   const int64_t chunks = (p.keep + kCompactRows - 1) / kCompactRows;
-  const int64_t fill = (6 * num_sms() + (int64_t)batch * kCompactSlices - 1) /
-                       ((int64_t)batch * kCompactSlices);
+  const int64_t slices = (int64_t)batch * kCompactSlices;
+  const int64_t fill = slices >= 2 * num_sms() ? 1 : (4 * num_sms() + slices - 1) / slices;
   p.splits = (int)std::min(chunks, fill);
   p.splits = p.splits >= 8 ? 8 : p.splits >= 4 ? 4 : p.splits >= 2 ? 2 : 1;
-  return (int64_t)batch * kCompactSlices * p.splits <= num_sms()
+  return slices * p.splits <= num_sms()
              ? launch_compact_kernel<2>(p, batch, stream)
              : launch_compact_kernel<1>(p, batch, stream);
 }

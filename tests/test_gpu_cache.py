@@ -368,6 +368,45 @@ def test_compact_moves_every_bit(paged, page, in_place, lens, keep):
         assert torch.equal(a, w)
 
 
+@pytest.mark.parametrize("batch,n,keep,paged,in_place", [
+    # in place, most tokens kept, so that what one chunk's rows are moved over is another's source;
+    # on 148 SMs: one CTA a slice and 20 chunks; clusters of two, four and eight and several chunks
+    (100, 5200, 5001, True, True), (100, 700, 513, False, True), (20, 6000, 5777, False, True),
+    (12, 9000, 8500, True, True), (4, 20000, 19500, False, True), (1, 40000, 39001, True, True),
+    # into other pages, two to four steps of a warp
+    (20, 1400, 1003, True, False), (20, 1300, 1150, False, False), (40, 1700, 1501, True, False),
+])
+def test_compact_many_sequences_and_chunks(batch, n, keep, paged, in_place):
+    kv, codes, scale, table, layout = _caches(batch, n, paged, 64, seed=batch)
+    mass = torch.rand(batch, n, device=DEV)
+    lens = [n - 3 * (b % 7) for b in range(batch)]
+    r = np.random.default_rng(keep)
+    kept = np.stack([np.sort(np.r_[0:5, 5 + r.permutation(m - 5)[:keep - 5]]) for m in lens])
+    kept, new = torch.from_numpy(kept.astype(np.int32)).cuda(), _i32([keep] * batch)
+    src = [t.clone() for t in (kv, codes, scale, mass)]
+    if in_place:
+        ttable, to = table, (kv, codes, scale, mass)
+        dsa.dsa_cache_compact(kv, codes, scale, layout(_i32(lens)), kept, new, mass=mass)
+    else:
+        tkv, tcodes, tscale, ttable, tlayout = _caches(batch, keep, paged, 64, seed=3)
+        to = (tkv, tcodes, tscale, torch.rand(batch, keep, device=DEV))
+        dsa.dsa_cache_compact(kv, codes, scale, layout(_i32(lens)), kept, new, mass, tlayout(None),
+                              *to)
+    torch.cuda.synchronize()
+    assert dsa.dsa_get_device_error() == 0
+    i = torch.arange(keep, device=DEV)
+    for b, m in enumerate(lens):
+        s = kept[b].long()
+        for x, y in zip(src[:3], to[:3]):
+            assert torch.equal(_rows(y, ttable, 64, b, i), _rows(x, table, 64, b, s)), f"sequence {b}"
+        assert torch.equal(to[3][b, :keep], src[3][b, s])
+        if in_place:
+            assert not to[3][b, keep:m].any() and torch.equal(to[3][b, m:], src[3][b, m:])
+            rest = torch.arange(keep, n, device=DEV)    # slots behind the new length as they were
+            for x, y in zip(src[:3], to[:3]):
+                assert torch.equal(_rows(y, table, 64, b, rest), _rows(x, table, 64, b, rest))
+
+
 def test_compact_into_fresh_pages_of_the_same_cache_without_mass():
     kv, codes, scale, table, layout = _caches(2, 300, True, 64, seed=9, extra=6)
     used = set(table.flatten().tolist())
