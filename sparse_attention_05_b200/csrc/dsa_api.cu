@@ -1011,7 +1011,7 @@ dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStre
     cache_move_kernel<<<(unsigned)((int64_t)batch * p.splits), kCompactThreads, 0, stream>>>(p);
     return cuda_status(cudaGetLastError());
   }
-  const int64_t chunks = (p.keep + kCompactRows - 1) / kCompactRows;
+  const int64_t chunks = (p.keep + kCompactRows - 1ll) / kCompactRows;
   const int64_t slices = (int64_t)batch * kCompactSlices;
   const int64_t fill = slices >= 2 * num_sms() ? 1 : (4 * num_sms() + slices - 1) / slices;
   p.splits = (int)std::min(chunks, fill);

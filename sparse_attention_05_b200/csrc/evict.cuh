@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2)
   }
   if (gtid == 0) p.new_lens[b] = min(n, p.keep);
   if (n <= p.keep) {
-    for (int i = gtid; i < p.keep; i += gthreads) kept[i] = i < n ? i : -1;
+    for (int64_t i = gtid; i < p.keep; i += gthreads) kept[i] = i < n ? (int)i : -1;  // keep + a stride: past 2^31
     return;
   }
   const int want = p.keep - p.sink - p.recent;  // of [sink, n - recent), which holds more

@@ -296,6 +296,24 @@ def test_select_in_large_batches(batch, ctx, keep, kind):
         assert torch.all(kept[b, len(want):] == -1)
 
 
+def test_keep_at_the_end_of_int32():
+    """kept of 8 GB, nearly all of it padding: its last places are counted in 64 bits."""
+    keep = 2**31 - 1
+    kept = torch.zeros(1, keep, dtype=torch.int32, device=DEV)
+    kv, codes, scale, _, layout = _caches(1, 600, False)
+    lay = layout(_i32([500]))
+    mass = torch.rand(1, 600, device=DEV)
+    _, new = dsa.dsa_evict_select(mass, lay, keep, sink=3, recent=5, kept=kept)
+    assert new.tolist() == [500] and kept[0, :500].tolist() == list(range(500))
+    assert int(kept[0, 500:].max()) == -1 and int(kept[0, 500:].min()) == -1
+    kept[0, :4] = _i32([7, 8, 11, 499])
+    before = [t.clone() for t in (kv, codes, scale, mass)]
+    dsa.dsa_cache_compact(kv, codes, scale, lay, kept, _i32([4]), mass=mass)
+    assert dsa.dsa_get_device_error() == 0
+    for a, b in zip((kv, codes, scale, mass), before):
+        assert torch.equal(a[0, :4], b[0, [7, 8, 11, 499]])
+
+
 def test_select_reports_a_length_out_of_range():
     m = torch.rand(3, 100, device=DEV)
     kept, new = dsa.dsa_evict_select(m, dsa.KvLayout(3, 100, _i32([101, -1, 90])), 10)
