@@ -33,6 +33,7 @@ constexpr int kDIdx = 128, kMaxK = 2048;
 std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
@@ -62,6 +63,7 @@ dsa_status_t check_geometry(const dsa_kv_desc_t* kv, const dsa_q_desc_t* q, Geom
     return DSA_ERR_INVALID_ARG;
   }
   if (q->q_per_seq > kv->max_ctx) return DSA_ERR_INVALID_ARG;
+  if (!aligned4(kv->seqlens) || !aligned4(q->q_start)) return DSA_ERR_INVALID_ARG;
   if (q->row_begin < 0 || q->row_begin >= q->q_per_seq || q->row_count < 0 ||
       q->row_count > q->q_per_seq - q->row_begin)
     return DSA_ERR_INVALID_ARG;
@@ -81,7 +83,8 @@ dsa_status_t check_geometry(const dsa_kv_desc_t* kv, const dsa_q_desc_t* q, Geom
   if (kv->layout == DSA_KV_CONTIGUOUS) {
     g->cache_rows = (int64_t)kv->batch * kv->max_ctx;
   } else if (kv->layout == DSA_KV_PAGED) {
-    if (!kv->block_table || kv->num_pages < 1 || kv->max_pages < 1) return DSA_ERR_INVALID_ARG;
+    if (!kv->block_table || !aligned4(kv->block_table) || kv->num_pages < 1 || kv->max_pages < 1)
+      return DSA_ERR_INVALID_ARG;
     if (kv->page_size < 64 || kv->page_size % 64 != 0) return DSA_ERR_UNSUPPORTED_SHAPE;
     if ((int64_t)kv->max_pages * kv->page_size < kv->max_ctx) return DSA_ERR_INVALID_ARG;
     g->block_table = kv->block_table;
@@ -1583,8 +1586,7 @@ dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_stride, con
   if ((int64_t)g.batch * g.row_count >= (1ll << 31)) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!latent_new || !k_new) return DSA_ERR_INVALID_ARG;
   if (!aligned16(latent_new) || !aligned16(k_new) || !aligned16(kv_cache) || !aligned16(k_idx) ||
-      (reinterpret_cast<uintptr_t>(k_scale) & 3) || (reinterpret_cast<uintptr_t>(freqs) & 7) ||
-      (reinterpret_cast<uintptr_t>(positions) & 3))
+      !aligned4(k_scale) || (reinterpret_cast<uintptr_t>(freqs) & 7) || !aligned4(positions))
     return DSA_ERR_INVALID_ARG;
   if (latent_stride < 576 || latent_stride % 8 || k_stride < 128 || k_stride % 8)
     return DSA_ERR_INVALID_ARG;
@@ -1644,7 +1646,7 @@ dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const dsa_kv_des
   if (!mass || !kv_cache) return DSA_ERR_INVALID_ARG;
   if (g.num_q == 0) return DSA_OK;
   if (!q || !idx || !lse) return DSA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(kv_cache) || (reinterpret_cast<uintptr_t>(mass) & 3))
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned4(mass) || !aligned4(idx) || !aligned4(lse))
     return DSA_ERR_INVALID_ARG;
   if (g.batch > 65535 || (int64_t)g.batch * g.row_count >= (1ll << 31))
     return DSA_ERR_UNSUPPORTED_SHAPE;
@@ -1667,9 +1669,7 @@ dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_d
   if (keep < 1 || sink < 0 || recent < 0 || sink > keep || recent > keep - sink)
     return DSA_ERR_INVALID_ARG;
   if (new_lens == kv->seqlens) return DSA_ERR_INVALID_ARG;  // read while it is written
-  if ((reinterpret_cast<uintptr_t>(mass) & 3) || (reinterpret_cast<uintptr_t>(kept) & 3) ||
-      (reinterpret_cast<uintptr_t>(new_lens) & 3))
-    return DSA_ERR_INVALID_ARG;
+  if (!aligned4(mass) || !aligned4(kept) || !aligned4(new_lens)) return DSA_ERR_INVALID_ARG;
   if (g.max_ctx > kEvictMaxCtx) return DSA_ERR_UNSUPPORTED_SHAPE;
   EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent, 1, 0};
   return launch_evict(p, g.batch, (cudaStream_t)stream);
@@ -1709,6 +1709,9 @@ dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, floa
   if (!aligned16(kv_cache) || !aligned16(k_idx) || !aligned16(dst_kv_cache) ||
       !aligned16(dst_k_idx))
     return DSA_ERR_INVALID_ARG;
+  for (const void* f : {(const void*)k_scale, (const void*)mass, (const void*)dst_k_scale,
+                        (const void*)dst_mass, (const void*)kept, (const void*)new_lens})
+    if (!aligned4(f)) return DSA_ERR_INVALID_ARG;
   CompactParams p{};
   p.kv = reinterpret_cast<const uint8_t*>(kv_cache);
   p.k_idx = reinterpret_cast<const uint8_t*>(k_idx);

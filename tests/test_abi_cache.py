@@ -185,6 +185,39 @@ def test_evict_and_compact_refusals(lib):
     assert com(**dict(to, dst=_kv(layout=1, page=32, pages=4, max_pages=16, bt=0x2000))) == 2
 
 
+ODD = 0x700002   # on no 4-byte boundary
+
+
+def test_four_byte_pointers_are_refused_off_their_boundary(lib):
+    odd = ctypes.c_void_p(ODD)
+    for name in ("idx", "lse", "mass"):
+        assert _mass(lib, **{name: odd}) == 1, name
+    kv = _kv()
+
+    def sel(mass=FAKE, kept=OTHER, lens=FAKE):
+        return lib.dsa_evict_select(mass, 512, by(kv), 8, 2, 3, kept, lens, None)
+    for name in ("mass", "kept", "lens"):
+        assert sel(**{name: odd}) == 1, name
+
+    def com(c=FAKE, mass=OTHER, kept=OTHER, lens=OTHER, dst=None, tc=None, tm=None):
+        to = None if dst is None else ctypes.c_void_p(0x1900000)
+        return lib.dsa_cache_compact(FAKE, FAKE, c, mass, 512, by(kv), kept, 8, lens,
+                                     by(dst) if dst else None, to, to, tc, tm, 512, None)
+    for name in ("c", "mass", "kept", "lens"):
+        assert com(**{name: odd}) == 1, name
+    far = ctypes.c_void_p(0x2900000)
+    for name in ("tc", "tm"):
+        assert com(**dict(dict(dst=_kv(), tc=far, tm=far), **{name: ctypes.c_void_p(0x2900002)})) == 1
+    # lengths, block table and row starts of any call
+    lens = _kv()
+    lens.seqlens = ODD
+    for name, desc in (("seqlens", lens),
+                       ("table", _kv(layout=1, page=64, pages=64, max_pages=8, bt=ODD))):
+        assert _append(lib, kv=desc) == 1 and _mass(lib, kv=desc) == 1, name
+    assert _append(lib, q=dsa.QDescC(2, 1, 0, 0, ODD)) == 1
+    assert _mass(lib, q=dsa.QDescC(2, 1, 0, 0, ODD)) == 1
+
+
 def test_binding_refuses_wrong_tensors():
     """Types, shapes and devices the pointers alone would not show."""
     x = torch.zeros(2, 4, 64)
