@@ -384,7 +384,9 @@ DSA_API dsa_status_t dsa_mha_prefill(const void* q_idx, const float* w, const vo
  * tokens enter both caches in the formats the path reads, every cached token's share
  * of the attention is accumulated, and caches are trimmed to the tokens that matter.
  * After a trim a token's slot is no longer its position in the text, so these calls
- * take rotary positions as an input of their own. */
+ * take rotary positions as an input of their own. What a call writes may share no memory
+ * with what it reads, nor two of its outputs with each other (DSA_ERR_INVALID_ARG), but
+ * where the call says so. */
 
 typedef enum { DSA_BF16 = 0, DSA_FP16 = 1, DSA_FP32 = 2 } dsa_dtype_t;
 
@@ -475,7 +477,7 @@ DSA_API dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const ds
  *  kv        batch, max_ctx (at most 2^22) and seqlens are used
  *  keep      >= 1 and >= sink + recent
  *  kept      int32 [batch][keep] out: the slots that stay, ascending, padded with -1
- *  new_lens  int32 [batch] out: min(seqlen, keep); not kv's seqlens array itself. */
+ *  new_lens  int32 [batch] out: min(seqlen, keep). */
 DSA_API dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_desc_t* kv,
                                       int32_t keep, int32_t sink, int32_t recent, int32_t* kept,
                                       int32_t* new_lens, dsa_stream_t stream);
@@ -492,7 +494,8 @@ DSA_API dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const 
  *  dst       NULL: in place (the dst pointers must be NULL, dst_mass_ld is ignored).
  *            Otherwise the geometry of the destination (batch as kv's, seqlens ignored),
  *            whose cache arrays may be the source's own as long as no destination slot
- *            is a slot of any source sequence (pages fresh from the pool; both paged).
+ *            is a slot of any source sequence (pages fresh from the pool; both paged, each
+ *            with its own table).
  *  dst_mass  fp32 [batch][dst_mass_ld], apart from mass; NULL where mass is
  * No two sequences may share the slots they are trimmed in. */
 DSA_API dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, float* mass,

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstring>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -39,6 +40,25 @@ inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_byt
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
 
+// A call's arrays (null or empty: none).
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && overlap(a.p, a.bytes, b.p, b.bytes);
+}
+// No written array shares memory with another, nor with one that is read.
+bool apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span* v = w + 1; v != written.end(); ++v)
+      if (overlap(*w, *v)) return false;
+    for (const Span& r : read)
+      if (overlap(*w, r)) return false;
+  }
+  return true;
+}
+
 dsa_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -52,6 +72,10 @@ struct Geometry {
   const int32_t* q_start;    // ragged query rows ([batch + 1], device) or nullptr
   int64_t cache_rows;  // rows of each per-token cache array
 };
+
+Span lens_of(const Geometry& g) { return {g.seqlens, (int64_t)g.batch * 4}; }
+Span table_of(const Geometry& g) { return {g.block_table, (int64_t)g.batch * g.max_pages * 4}; }
+Span starts_of(const Geometry& g) { return {g.q_start, (g.batch + 1ll) * 4}; }
 
 dsa_status_t check_geometry(const dsa_kv_desc_t* kv, const dsa_q_desc_t* q, Geometry* g) {
   if (!kv || !q) return DSA_ERR_INVALID_ARG;
@@ -866,6 +890,9 @@ dsa_status_t launch_rope(const void* x, const int32_t* positions, const double* 
   const bool same = (d->num_rows == 1 || strides[0] == strides[2]) &&
                     (d->heads == 1 || strides[1] == strides[3]);
   const bool in_place = xa == oa && same;
+  if (!apart({{out, os.extent * es}},
+             {{positions, d->num_rows * 4}, {freqs, (int64_t)d->rot_dim / 2 * 8}}))
+    return DSA_ERR_INVALID_ARG;
   if (!in_place && xa < oa + os.extent * es && oa < xa + xs.extent * es) {
     // interleaved views of one buffer: every row of one between two rows of the other
     if (!same || os.inner_n < 2 || (oa > xa ? oa - xa : xa - oa) % es) return DSA_ERR_INVALID_ARG;
@@ -1592,9 +1619,10 @@ dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_stride, con
     return DSA_ERR_INVALID_ARG;
   // a row written might be another's, not yet read
   if (latent_stride > (1ll << 30) || k_stride > (1ll << 30) ||
-      overlap(latent_new, ((int64_t)(g.num_q - 1) * latent_stride + 576) * 2, kv_cache,
-              g.cache_rows * 1152) ||
-      overlap(k_new, ((int64_t)(g.num_q - 1) * k_stride + 128) * 2, k_idx, g.cache_rows * 128))
+      !apart({{kv_cache, g.cache_rows * 1152}, {k_idx, g.cache_rows * 128}, {k_scale, g.cache_rows * 4}},
+             {{latent_new, ((int64_t)(g.num_q - 1) * latent_stride + 576) * 2},
+              {k_new, ((int64_t)(g.num_q - 1) * k_stride + 128) * 2},
+              {positions, (int64_t)g.num_q * 4}, {freqs, 32 * 8}, lens_of(g), table_of(g), starts_of(g)}))
     return DSA_ERR_INVALID_ARG;
   AppendParams p{};
   p.latent = reinterpret_cast<const __nv_bfloat16*>(latent_new);
@@ -1654,6 +1682,11 @@ dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const dsa_kv_des
   if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
                workspace_bytes < need))
     return DSA_ERR_WORKSPACE;
+  if (!apart({{mass, ((g.batch - 1) * mass_ld + g.max_ctx) * 4}, {workspace, (int64_t)need}},
+             {{q, (int64_t)g.num_q * kMassHeads * kMassDqk * 2}, {kv_cache, g.cache_rows * 1152},
+              {idx, (int64_t)g.num_q * k * 4}, {lse, (int64_t)g.num_q * kMassHeads * 4}, lens_of(g),
+              table_of(g), starts_of(g)}))
+    return DSA_ERR_INVALID_ARG;
   return launch_attn_mass(q, kv_cache, g, idx, k, scale, lse, mass, mass_ld, workspace,
                           (cudaStream_t)stream);
 }
@@ -1668,9 +1701,12 @@ dsa_status_t dsa_evict_select(const float* mass, int64_t mass_ld, const dsa_kv_d
   if (!mass || !kept || !new_lens || mass_ld < g.max_ctx) return DSA_ERR_INVALID_ARG;
   if (keep < 1 || sink < 0 || recent < 0 || sink > keep || recent > keep - sink)
     return DSA_ERR_INVALID_ARG;
-  if (new_lens == kv->seqlens) return DSA_ERR_INVALID_ARG;  // read while it is written
   if (!aligned4(mass) || !aligned4(kept) || !aligned4(new_lens)) return DSA_ERR_INVALID_ARG;
   if (g.max_ctx > kEvictMaxCtx) return DSA_ERR_UNSUPPORTED_SHAPE;
+  // a sequence's CTAs read its mass again, and others their lengths, after the first writes
+  if (!apart({{kept, (int64_t)g.batch * keep * 4}, {new_lens, (int64_t)g.batch * 4}},
+             {{mass, ((g.batch - 1) * mass_ld + g.max_ctx) * 4}, lens_of(g)}))
+    return DSA_ERR_INVALID_ARG;
   EvictParams p{mass, g.seqlens, kept, new_lens, mass_ld, g.max_ctx, keep, sink, recent, 1, 0};
   return launch_evict(p, g.batch, (cudaStream_t)stream);
 }
@@ -1695,15 +1731,6 @@ dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, floa
     if (st != DSA_OK) return st;
     if (!dst_kv_cache || !dst_k_idx || !dst_k_scale || !mass != !dst_mass)
       return DSA_ERR_INVALID_ARG;
-    // the chunks move in no order: the same slots would be read after they are written
-    const bool own_pages = g.block_table && t.block_table && g.block_table != t.block_table;
-    if (!own_pages && (overlap(kv_cache, g.cache_rows * 1152, dst_kv_cache, t.cache_rows * 1152) ||
-                       overlap(k_idx, g.cache_rows * 128, dst_k_idx, t.cache_rows * 128) ||
-                       overlap(k_scale, g.cache_rows * 4, dst_k_scale, t.cache_rows * 4)))
-      return DSA_ERR_INVALID_ARG;
-    if (mass && mass < dst_mass + (int64_t)t.batch * dst_mass_ld &&
-        dst_mass < mass + (int64_t)g.batch * mass_ld)
-      return DSA_ERR_INVALID_ARG;
   }
   if (mass && (mass_ld < g.max_ctx || dst_mass_ld < t.max_ctx)) return DSA_ERR_INVALID_ARG;
   if (!aligned16(kv_cache) || !aligned16(k_idx) || !aligned16(dst_kv_cache) ||
@@ -1712,6 +1739,23 @@ dsa_status_t dsa_cache_compact(void* kv_cache, void* k_idx, float* k_scale, floa
   for (const void* f : {(const void*)k_scale, (const void*)mass, (const void*)dst_k_scale,
                         (const void*)dst_mass, (const void*)kept, (const void*)new_lens})
     if (!aligned4(f)) return DSA_ERR_INVALID_ARG;
+  const Span from[4] = {{kv_cache, g.cache_rows * 1152}, {k_idx, g.cache_rows * 128},
+                        {k_scale, g.cache_rows * 4}, {mass, ((g.batch - 1) * mass_ld + g.max_ctx) * 4}};
+  const Span to[4] = {{dst_kv_cache, t.cache_rows * 1152}, {dst_k_idx, t.cache_rows * 128},
+                      {dst_k_scale, t.cache_rows * 4}, {dst_mass, ((t.batch - 1) * dst_mass_ld + t.max_ctx) * 4}};
+  if (!apart({to[0], to[1], to[2], to[3]},
+             {{kept, (int64_t)g.batch * keep * 4}, {new_lens, (int64_t)g.batch * 4}, lens_of(g),
+              table_of(g), table_of(t)}))
+    return DSA_ERR_INVALID_ARG;
+  if (dst) {
+    // the rows move in no order: the same slots would be read after they are written. Arrays
+    // of pages may be the source's own, with other pages in another table.
+    const bool own_pages = g.block_table && t.block_table && g.block_table != t.block_table;
+    for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < 4; ++j)
+        if (overlap(from[i], to[j]) && !(own_pages && i == j && i < 3 && from[i].p == to[j].p))
+          return DSA_ERR_INVALID_ARG;
+  }
   CompactParams p{};
   p.kv = reinterpret_cast<const uint8_t*>(kv_cache);
   p.k_idx = reinterpret_cast<const uint8_t*>(k_idx);

@@ -218,6 +218,91 @@ def test_four_byte_pointers_are_refused_off_their_boundary(lib):
     assert _mass(lib, q=dsa.QDescC(2, 1, 0, 0, ODD)) == 1
 
 
+def _at(v):
+    return ctypes.c_void_p(v)
+
+
+def test_outputs_that_overlap_what_is_read_are_refused(lib):
+    """One byte range into another, at both ends (the library writes some of its outputs before it
+    has read all of its inputs)."""
+    kv = _kv()
+    kv.seqlens = 0x50000
+    paged = _kv(layout=1, page=64, pages=16, max_pages=8, bt=0x60000)
+
+    def sel(mass=0x1000000, kept=0x2000000, lens=0x3000000):
+        return lib.dsa_evict_select(_at(mass), 600, by(kv), 8, 2, 3, _at(kept), _at(lens), None)
+    size = (600 + 512) * 4                              # two rows, the second to max_ctx
+    assert sel(kept=0x1000000) == 1 and sel(kept=0x1000000 + size - 4) == 1
+    assert sel(kept=0x1000000 - 2 * 8 * 4 + 4) == 1
+    assert sel(lens=0x1000000 + size - 4) == 1
+    assert sel(lens=0x50004) == 1 and sel(lens=0x50000 - 4) == 1   # shifted against the lengths
+    assert sel(kept=0x50004) == 1
+    assert sel(kept=0x3000000 - 8 * 4) == 1 and sel(lens=0x2000000 + 2 * 8 * 4 - 4) == 1
+    # what does not overlap is not refused for it (there is no GPU: the launch fails, or the GPU
+    # of a GPU machine is not asked)
+    if not torch.cuda.is_available():
+        assert sel(kept=0x1000000 + size) == 3 and sel(lens=0x50008) == 3
+
+    # append: any of the three caches over any input
+    caches = dict(kvc=_at(0x1000000), ki=_at(0x2000000), sc=_at(0x3000000))
+    ins = dict(lat=_at(0x4000000), key=_at(0x5000000), pos=_at(0x6000000), f=_at(0x7000000))
+
+    def app(desc=None, q=None, **kw):
+        return _append(lib, kv=desc or _kv(), q=q, **dict(dict(caches, **ins), **kw))
+    ends = dict(kvc=1024 * 1152, ki=1024 * 128, sc=1024 * 4)
+    for c, n in ends.items():
+        for i in ins:
+            assert app(**{i: _at(caches[c].value + n - 16)}) == 1, (c, i)
+        other = [o for o in ends if o != c][0]
+        assert app(**{other: _at(caches[c].value + n - 16)}) == 1, c
+    lens = _kv()
+    lens.seqlens = 0x3000000 + 1024 * 4 - 4
+    assert app(lens) == 1
+    assert app(_kv(layout=1, page=64, pages=16, max_pages=8, bt=0x3000000 - 60)) == 1
+    assert app(q=dsa.QDescC(2, 1, 0, 0, 0x3000000 - 8)) == 1
+
+    # mass and workspace over the inputs and each other
+    far = dict(qp=_at(0x10000000), kvc=_at(0x20000000), idx=_at(0x30000000), lse=_at(0x40000000),
+               mass=_at(0x50000000), ws=_at(0x60000000), q=dsa.QDescC(4, 2, 0, 0))
+    ends = dict(qp=4 * 147456, kvc=1024 * 1152, idx=4 * 16 * 4, lse=4 * 512)
+    for name, n in ends.items():
+        assert _mass(lib, **dict(far, mass=_at(far[name].value + n - 4))) == 1, name
+        assert _mass(lib, **dict(far, ws=_at(far[name].value))) == 1, name
+    assert _mass(lib, **dict(far, mass=_at(0x60000000))) == 1
+    assert _mass(lib, **dict(far, kv=lens, mass=_at(lens.seqlens - 4))) == 1
+
+    # rope: the output over positions and frequencies
+    d = _rope()
+    assert _call_rope(lib, d, pos=_at(OTHER.value + 3 * 384 * 2 - 4)) == 1
+    assert _call_rope(lib, d, f=OTHER) == 1
+
+    # compact: what is moved to over the lists, the lengths, the tables and the other arrays
+    def com(a=0x1000000, b=0x2000000, c=0x3000000, mass=0x4000000, kept=0x5000000, lens=0x6000000,
+            geometry=None, dst=None, to=(None,) * 4):
+        return lib.dsa_cache_compact(_at(a), _at(b), _at(c), _at(mass), 512, by(geometry or kv),
+                                     _at(kept), 8, _at(lens), by(dst) if dst else None,
+                                     *(_at(t) for t in to), 512, None)
+    ends = (0x1000000 + 1024 * 1152, 0x2000000 + 1024 * 128, 0x3000000 + 1024 * 4,
+            0x4000000 + 1024 * 4)
+    for end in ends:
+        assert com(kept=end - 4) == 1 and com(lens=end - 4) == 1
+        moved = _kv()
+        moved.seqlens = end - 4
+        assert com(geometry=moved) == 1
+        assert com(geometry=_kv(layout=1, page=64, pages=16, max_pages=8, bt=end - 4)) == 1
+    assert com(b=ends[0] - 16) == 1 and com(c=ends[1] - 4) == 1 and com(mass=ends[2] - 4) == 1
+    to = (0x11000000, 0x12000000, 0x13000000, 0x14000000)
+    other = _kv(layout=1, page=64, pages=16, max_pages=8, bt=0x70000)
+    for i, start in enumerate(to):
+        assert com(geometry=paged, dst=other, to=to, kept=start) == 1
+        assert com(geometry=paged, dst=other, to=to, lens=start + 4) == 1
+        for j, end in enumerate(ends):     # into its own arrays only as they are
+            cross = to[:i] + (end - 16,) + to[i + 1:]
+            assert com(geometry=paged, dst=other, to=cross) == 1, (i, j)
+    table = _kv(layout=1, page=64, pages=16, max_pages=8, bt=to[2] + 64)
+    assert com(geometry=paged, dst=table, to=to) == 1
+
+
 def test_binding_refuses_wrong_tensors():
     """Types, shapes and devices the pointers alone would not show."""
     x = torch.zeros(2, 4, 64)
