@@ -461,7 +461,8 @@ DSA_API dsa_status_t dsa_cache_append(const void* latent_new, int64_t latent_str
  *  workspace  device, 256-byte aligned, dsa_attn_mass_workspace_size() bytes (0 for one
  *         row a sequence: then it may be NULL); written during the call (stream order),
  *         nothing kept in it. Many rows (for the
- *         caches' size) are summed in units of 2^-40, a few in fp32. */
+ *         caches' size) are summed as integers, in units of 2^-56 times row_count rounded up
+ *         to a power of two (a slot may then take up to 64 from each row), a few in fp32. */
 DSA_API size_t dsa_attn_mass_workspace_size(const dsa_kv_desc_t* kv, const dsa_q_desc_t* q,
                                             int32_t k);
 DSA_API dsa_status_t dsa_attn_mass(const void* q, const void* kv_cache, const dsa_kv_desc_t* kv,

@@ -40,8 +40,9 @@
 //     row carry equal p, so their order is free);
 //   few rows a sequence: p goes to the workspace, and one CTA a sequence adds its rows
 //     one after another;
-//   many rows: p is added as a 64-bit integer in units of 2^-40, which commutes, and a
-//     second kernel turns the sums into fp32. 2^-41 is the most an entry is off.
+//   many rows: p is added as a 64-bit integer, which commutes, and a second kernel turns the
+//     sums into fp32. The unit is the smallest in which the rows' largest weights add up below
+//     2^62 (2^-47 for 512 rows); half of it is the most an entry is off.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -67,7 +68,6 @@ constexpr int kMassSmemBytes = 1024 + kMassStages * kMassStageBytes + kMassQByte
 static_assert(kMassSmemBytes <= 232448, "attention mass shared memory exceeds the per-CTA limit");
 static_assert(kMassQCols + kMassMaxTile <= 512, "tensor memory");
 static_assert(kMassStages < kMassChunks, "Q's last chunk is free once its place in the ring is");
-constexpr float kMassUnit = 1099511627776.0f;             // 2^40 units of fixed point
 constexpr float kMassMaxP = 64.0f;                        // a larger p is not a weight
 // The tensor core truncates its running sums: after the 36 dependent steps of a logit it is
 // short of 2^-21 of itself on average (measured 4.4e-7 to 5.3e-7 for logits of either sign
@@ -96,6 +96,7 @@ struct MassParams {
   int32_t ntiles;              // of a row
   int32_t whole_rows;          // CTAs take whole rows instead of runs of tiles
   float scale;
+  float units;                 // of the integer sums in 1: a power of two
   uint64_t timeout_ns;
 };
 
@@ -518,7 +519,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         if (!p.sums)
           atomicAdd(p.mass + (int64_t)now.b * p.mass_ld + slot, weight);
         else if (w <= kMassMaxP)
-          atomicAdd(s, (unsigned long long)__float2ll_rn(w * kMassUnit));
+          atomicAdd(s, (unsigned long long)__float2ll_rn(w * p.units));
         else
           atomicOr(s, kMassNan);
       }
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(256) mass_add_sums_kernel(const __grid_constan
   if (s == 0) return;
   float* m = p.mass + (int64_t)b * p.mass_ld + i;
   *m = s & kMassNan ? __int_as_float(0x7fffffff)
-                    : *m + (float)((double)s * (1.0 / (double)kMassUnit));
+                    : *m + (float)((double)s / (double)p.units);
 }
 
 }  // namespace dsa

@@ -1108,6 +1108,9 @@ dsa_status_t launch_attn_mass(const void* q, const void* kv_cache, const Geometr
   p.max_pages = g.max_pages;
   p.num_pages = g.num_pages;
   p.scale = (float)(scale * kMassUntruncate);
+  int bits = 62;  // of a slot's sum: row_count weights of at most kMassMaxP
+  while (std::ldexp((double)kMassMaxP * g.row_count, bits) > std::ldexp(1.0, 62)) --bits;
+  p.units = std::ldexp(1.0f, bits);
   p.timeout_ns = g_timeout_ns.load();
   if (p.sums) {
     const cudaError_t e = cudaMemsetAsync(workspace, 0, (size_t)g.batch * g.max_ctx * 8, stream);

@@ -250,3 +250,39 @@ def test_long_prefill_agrees_with_its_windows(k):
     assert dsa.dsa_get_device_error() == 0
     assert torch.all((whole - parts).abs() <= 27 * 2.0 ** -24 * parts)
     assert abs(float(whole.double().sum()) - L) <= L * 1e-4   # the LSE's tolerance a row
+
+
+@pytest.mark.parametrize("rows", [16, 100])
+def test_many_rows_keep_small_weights(rows):
+    """Every weight of the window below 2^-41 (an LSE far above the logits): summed as integers in
+    units of 2^-56 times the rows, rounded up to a power of two. Half a unit an entry, beside what
+    test_gpu_attn_mass's header gives for the weight itself."""
+    ctx, k = 400, 150
+    p = synth.ragged([ctx], [rows], seed=92)
+    idx = _idx(p, k, 13)
+    g = p.to(DEV)
+    lay = dsa.KvLayout.of(g)
+    assert dsa.dsa_attn_mass_workspace_size(lay, rows, rows, k, q_start=g.q_start) == 256 * -(-ctx * 8 // 256)
+    a = oracle_args(p)
+    q = np.asarray(a["q"], np.float64)
+    c = np.asarray(resolve_kv_rows(a["kv"], 0, list(range(ctx)), a["block_table"], p.page_size),
+                   np.float64)
+    z = p.scale * np.einsum("thd,sd->ths", q, c)
+    lse = (z.max(2) + 27.0).astype(np.float32)
+    unit = 2.0 ** (np.ceil(np.log2(rows)) - 56)
+    want, tol = np.zeros(ctx), np.zeros(ctx)
+    for t in range(rows):
+        sel = idx[t][idx[t] >= 0]
+        w = np.exp(z[t][:, sel] - lse[t][:, None].astype(np.float64))
+        dz = 2 * 576 * 2.0 ** -24 * p.scale * (np.abs(q[t]) @ np.abs(c[sel]).T) + \
+            (np.abs(z[t][:, sel]) + np.abs(lse[t])[:, None]) * 2.0 ** -22 + 2.0 ** -21
+        want[sel] += w.mean(0)
+        tol[sel] += (w * np.expm1(dz)).mean(0) + w.mean(0) * 130 * 2.0 ** -24 + unit / 2
+        assert w.mean(0).max() < 2.0 ** -41
+    mass = torch.zeros(1, p.max_ctx, device=DEV)
+    dsa.dsa_attn_mass(g.q, g.kv, lay, rows, torch.from_numpy(idx).cuda(), p.scale,
+                      torch.from_numpy(lse).cuda(), mass, q_start=g.q_start)
+    assert dsa.dsa_get_device_error() == 0
+    got = mass[0, :ctx].double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= tol + np.abs(want) * 2.0 ** -23)
+    assert np.count_nonzero(got) > ctx // 2
