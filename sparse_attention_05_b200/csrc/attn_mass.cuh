@@ -69,10 +69,13 @@ static_assert(kMassSmemBytes <= 232448, "attention mass shared memory exceeds th
 static_assert(kMassQCols + kMassMaxTile <= 512, "tensor memory");
 static_assert(kMassStages < kMassChunks, "Q's last chunk is free once its place in the ring is");
 constexpr float kMassMaxP = 64.0f;                        // a larger p is not a weight
-// The tensor core truncates its running sums: after the 36 dependent steps of a logit it is
-// short of 2^-21 of itself on average (measured 4.4e-7 to 5.3e-7 for logits of either sign
-// and of standard deviations from 0.2 to 3). The scale makes up for the mean of it, which
-// would leave every weight 1e-6 too small.
+// The tensor core truncates its running sums: after the 36 dependent steps of a logit z it is
+// short of about 2^-21 z, and the weight off by as much. The scale makes up for the mean of it.
+// Against exp(scale q.c - LSE) for the LSE as it is given, rows whose weights' mean logit is
+// 2.2, 5.9, -1.3 and 19.8 are off by 2e-8, -3e-7, 1e-8 and -8e-7 of their weight, and by
+// -1.0e-6, -3.0e-6, 6e-7 and -9.7e-6 without. (The forward's LSE has truncated logits of its
+// own, in sums of 18 steps: its rows add up to 1 within 1e-6 either way.) Where partial sums
+// cancel, what is lost goes with them and no factor helps: 1.4e-5 with sums up to 29.
 constexpr double kMassUntruncate = 1.0 + 1.0 / 2097152.0;
 constexpr unsigned long long kMassNan = 1ull << 63;       // set, never added
 

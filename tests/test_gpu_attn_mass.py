@@ -286,3 +286,62 @@ def test_many_rows_keep_small_weights(rows):
     got = mass[0, :ctx].double().cpu().numpy()
     assert np.all(np.abs(got - want) <= tol + np.abs(want) * 2.0 ** -23)
     assert np.count_nonzero(got) > ctx // 2
+
+
+@pytest.mark.parametrize("kind", ["spread", "positive", "negative", "large"])
+def test_mean_error_of_the_weights(kind):
+    """The tensor core truncates a logit's running sum, so without a correction every weight would
+    be off the same way: by 2^-21 z as measured (z its logit), in the mean over a row 2^-21 of the
+    weights' mean logit. At most half of that may be left, beside 2^-23 for the LSE, the difference
+    and the exponential, whose roundings have no such direction. For an exactly rounded LSE and
+    for the forward's own: the formula takes the LSE as it is given."""
+    B, ctx, k, scale = 16, 3000, 2048, 576 ** -0.5
+    g = torch.Generator(device=DEV).manual_seed(93)
+    q = torch.randn(B, 128, 576, device=DEV, generator=g) * (12.0 if kind == "large" else 3.0)
+    kv = torch.randn(B, ctx, 576, device=DEV, generator=g) * 0.5
+    if kind in ("positive", "negative"):
+        q = q + (0.5 if kind == "positive" else -0.5)
+        kv = kv + 0.3
+    q, kv = q.bfloat16(), kv.bfloat16()
+    idx = torch.rand(B, ctx, device=DEV, generator=g).topk(k, dim=1).indices.sort(dim=1).values.int()
+    lay = dsa.KvLayout(B, ctx)
+    _, own = dsa.dsa_sparse_mla_fwd(q, kv, lay, 1, idx, scale)
+    z = torch.stack([q[b].double() @ kv[b][idx[b].long()].double().T for b in range(B)]) * scale
+    exact = torch.logsumexp(z, 2)
+    mean_z = float((torch.exp(z - exact[..., None]) * z).sum(2).mean())
+    for lse in (exact.float(), own):
+        mass = torch.zeros(B, ctx, device=DEV)
+        dsa.dsa_attn_mass(q, kv, lay, 1, idx, scale, lse, mass)
+        got = mass.gather(1, idx.long()).double()
+        want = torch.exp(z - lse.double()[..., None]).mean(1)
+        off = float((got.sum() - want.sum()) / want.sum())
+        assert abs(off) <= 2.0 ** -22 * abs(mean_z) + 2.0 ** -23
+        # the forward's logits are truncated too, in sums of their own
+        rows = got.sum(1) - 1
+        assert float(rows.mean().abs()) <= 2.0 ** -20 * abs(mean_z) + 2.0 ** -22
+    assert abs(mean_z) > 1
+    assert dsa.dsa_get_device_error() == 0
+
+
+def test_weights_of_cancelling_logits():
+    """Partial sums far above the logit they end at: what is lost goes with the partial sums. 36
+    steps of at most 2^-23 of the largest."""
+    B, ctx, k, scale = 4, 600, 512, 576 ** -0.5
+    g = torch.Generator(device=DEV).manual_seed(94)
+    up = torch.cat([torch.ones(288, device=DEV), -torch.ones(288, device=DEV)])
+    q = (torch.randn(B, 128, 576, device=DEV, generator=g) + 2.0).bfloat16()
+    kv = (torch.randn(B, ctx, 576, device=DEV, generator=g) * 0.5 + up).bfloat16()
+    idx = torch.rand(B, ctx, device=DEV, generator=g).topk(k, dim=1).indices.sort(dim=1).values.int()
+    rows = torch.stack([kv[b][idx[b].long()] for b in range(B)]).double()
+    z = torch.einsum("bhd,bsd->bhs", q.double(), rows) * scale
+    part = torch.einsum("bhd,bsd->bhs", q[..., :288].double(), rows[..., :288]).abs() * scale
+    lse = torch.logsumexp(z, 2).float()
+    mass = torch.zeros(B, ctx, device=DEV)
+    dsa.dsa_attn_mass(q, kv, dsa.KvLayout(B, ctx), 1, idx, scale, lse, mass)
+    terms = torch.exp(z - lse.double()[..., None])
+    want = terms.mean(1)
+    off = (36 * 2.0 ** -23 * 1.25 * part.amax() + z.abs() * 2.0 ** -21 + lse.abs()[..., None] * 2.0 ** -22
+           + 2.0 ** -21)
+    tol = (terms * torch.expm1(off)).mean(1) + want * 131 * 2.0 ** -24
+    err = (mass.gather(1, idx.long()).double() - want).abs()
+    assert float(part.mean()) > 5 * float(z.abs().mean()) and torch.all(err <= tol)
