@@ -404,7 +404,8 @@ typedef struct {
   int32_t heads, dim;     /* heads <= 65535, dim <= 32768                               */
   int32_t rot_begin;      /* first rotated dim of a head                                */
   int32_t rot_dim;        /* rotated dims: even, 2..512, rot_begin + rot_dim <= dim     */
-  float magnitude;        /* factor on the rotated dims (1, or YaRN's attention factor) */
+  float magnitude;        /* factor on the rotated dims (1 where a schedule scales the
+                             whole logit and a head has other dims too: see scale)     */
   int64_t num_rows;
   int64_t x_row_stride, x_head_stride, out_row_stride, out_head_stride;
 } dsa_rope_desc_t;
@@ -437,7 +438,8 @@ DSA_API dsa_status_t dsa_rope_bwd(const void* dout, const int32_t* positions, co
  *  latent_new  bf16 [T] rows of 576, latent_stride elements apart (a multiple of 8, at most 2^30)
  *  k_new       bf16 [T] rows of 128, k_stride elements apart (a multiple of 8, at most 2^30)
  *  positions   int32 [T] rotary positions, or NULL for the slots
- *  freqs       fp64 [32], magnitude as in dsa_rope
+ *  freqs       fp64 [32], magnitude as in dsa_rope (YaRN's factor m on queries and keys is
+ *              for whole heads: here magnitude = 1 and scale * m^2 in the attention)
  *  kv_cache, k_idx, k_scale  the caches, as dsa_sparse_mla_fwd and dsa_indexer_scores
  *              read them, apart from the new rows; no two rows of the window may share a
  *              slot. */

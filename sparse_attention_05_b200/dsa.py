@@ -538,14 +538,19 @@ D_ROPE = 64
 def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
                factor: float = 1.0, original_ctx: int = 4096, beta_fast: float = 32.0,
                beta_slow: float = 1.0, device=None) -> Tuple[torch.Tensor, float]:
-    """Radians per position of each pair (fp64 [rot_dim / 2]) and the magnitude that goes
-    with them, for ``dsa_rope`` and ``dsa_cache_append``. With theta_i = base^(-2i / rot_dim):
+    """Radians per position of each pair (fp64 [rot_dim / 2]), for ``dsa_rope`` and
+    ``dsa_cache_append``, and the schedule's factor m on queries and keys. With
+    theta_i = base^(-2i / rot_dim):
       None      theta_i
       "linear"  theta_i / factor (position interpolation)
       "ntk"     the same for base * factor^(rot_dim / (rot_dim - 2))
       "yarn"    g_i theta_i + (1 - g_i) theta_i / factor, g_i rising linearly from 0 at
-                beta_slow to 1 at beta_fast turns over original_ctx positions, and the
-                magnitude 0.1 ln(factor) + 1 (YaRN, arXiv 2309.00071, section 3)
+                beta_slow to 1 at beta_fast turns over original_ctx positions, and
+                m = 0.1 ln(factor) + 1 (YaRN, arXiv 2309.00071, section 3)
+    m scales the whole logit by m^2. Heads that rotate in all their dims may have it from
+    the calls' ``magnitude``; MLA's and the indexer's rotate in a part of theirs, so there
+    ``magnitude`` stays 1 and the attention's scale becomes scale * m**2 (the indexer's
+    selection does not depend on it).
     Any other schedule is a tensor of one's own."""
     if rot_dim < 2 or rot_dim % 2 or base <= 0 or factor <= 0 or original_ctx < 1:
         raise ValueError("rope_freqs: rot_dim must be even and base, factor, original_ctx positive")
@@ -671,7 +676,8 @@ def dsa_rope(x, positions, freqs, out=None, rot_begin: int = 0, interleaved: boo
              magnitude: float = 1.0, stream=None) -> torch.Tensor:
     """Rotary positions on dims [rot_begin, rot_begin + 2 len(freqs)) of every head of x
     [rows, dim] or [rows, heads, dim] (strided views allowed); ``out=x`` works in place.
-    positions int32 [rows]; freqs, magnitude as ``rope_freqs`` gives them (include/dsa.h)."""
+    positions int32 [rows]; freqs, magnitude a factor on those dims (include/dsa.h,
+    ``rope_freqs``)."""
     return _rope("dsa_rope", x, positions, freqs, out, rot_begin, interleaved, magnitude, stream)
 
 

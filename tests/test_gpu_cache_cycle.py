@@ -162,3 +162,43 @@ def test_two_streams_at_once():
 
     for a, b in zip(run(False), run(True)):
         assert torch.equal(a, b)
+
+
+def test_yarn_scales_the_whole_logit():
+    """A decode step under YaRN as ``rope_freqs`` says: only 64 of a logit's 576 dims rotate, so
+    its factor goes into the scale. The same factor on the rotated dims is another attention."""
+    n = 90
+    g = torch.Generator(device=DEV).manual_seed(12)
+    freqs, m = dsa.rope_freqs(64, scaling="yarn", factor=40.0, device=DEV)
+    scale = 192 ** -0.5
+    lat = (torch.randn(n, 576, generator=g, device=DEV) * 0.5).bfloat16()
+    key = torch.randn(n, 128, generator=g, device=DEV).bfloat16()
+    raw = torch.randn(1, 128, 576, generator=g, device=DEV).bfloat16()
+    lay, at = dsa.KvLayout(1, n), torch.tensor([n - 1], device=DEV, dtype=torch.int32)
+    idx = torch.arange(n, device=DEV, dtype=torch.int32)[None]
+    fn = freqs.cpu().numpy()
+    # the definition: rotate without a factor, multiply the logits by m^2
+    rows = rope_rows(lat.double().cpu().numpy()[:, None], range(n), fn, rot_begin=512,
+                     interleaved=True)[:, 0]
+    q64 = rope_rows(raw.double().cpu().numpy(), [n - 1], fn, rot_begin=512, interleaved=True)
+    want, lse64 = sparse_mla_token(q64[0], rows, scale * m * m, 512)
+    lses = []
+    for magnitude, factor in ((1.0, m * m), (m, 1.0)):
+        kv = torch.zeros(1, n, 576, device=DEV, dtype=torch.bfloat16)
+        codes = torch.zeros(1, n, 128, device=DEV, dtype=torch.uint8)
+        dsa.dsa_cache_append(lat, key, kv, codes, torch.zeros(1, n, device=DEV), lay, n, freqs,
+                             magnitude=magnitude)
+        q = dsa.dsa_rope(raw, at, freqs, rot_begin=512, interleaved=True, magnitude=magnitude)
+        out, lse = dsa.dsa_sparse_mla_fwd(q, kv, lay, 1, idx, scale * factor)
+        assert dsa.dsa_get_device_error() == 0
+        lses.append(lse[0].double().cpu().numpy())
+        if magnitude == 1.0:
+            # beside the kernel's own tolerances: the 64 rotated dims rounded to bf16 on both
+            # sides move a logit by at most 2 * 2^-8 (1 + 2^-8) sum |q_d c_d|
+            d = 2.0 ** -7 * 1.01 * scale * m * m * (np.abs(q64[0, :, 512:]) @ np.abs(rows[:, 512:]).T).max(1)
+            assert np.all(np.abs(lses[0] - lse64) <= LSE_ATOL + d)
+            err = np.abs(out[0].double().cpu().numpy() - want)
+            spread = np.abs(rows[:, :512]).max()
+            assert np.all(err <= OUT_ATOL + np.expm1(2 * d)[:, None] * spread)
+    d = 2.0 ** -7 * 1.01 * scale * m * m * (np.abs(q64[0, :, 512:]) @ np.abs(rows[:, 512:]).T).max(1)
+    assert np.abs(lses[1] - lse64).max() > 5 * d.max()
