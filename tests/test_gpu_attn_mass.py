@@ -345,3 +345,43 @@ def test_weights_of_cancelling_logits():
     tol = (terms * torch.expm1(off)).mean(1) + want * 131 * 2.0 ** -24
     err = (mass.gather(1, idx.long()).double() - want).abs()
     assert float(part.mean()) > 5 * float(z.abs().mean()) and torch.all(err <= tol)
+
+
+@pytest.mark.parametrize("lens,rows,k", [([1300, 1250], [1300, 1250], 40),
+                                         ([900, 700, 1000], [900, 0, 1000], 300)])
+def test_whole_prompts_against_the_formula(lens, rows, k):
+    """Rows enough for CTAs to take whole ones in turn (sixteen an SM: 2368 on 148), ragged, in fp64
+    on the GPU; in test_gpu_attn_mass's bounds."""
+    batch, ctx, scale = len(lens), max(lens), 576 ** -0.5
+    per = max(rows)
+    g = torch.Generator(device=DEV).manual_seed(95)
+    T = sum(rows)
+    start = np.concatenate([[0], np.cumsum(rows)])
+    q = (torch.randn(T, 128, 576, device=DEV, generator=g) * 2).bfloat16()
+    kv = (torch.randn(batch, ctx, 576, device=DEV, generator=g) * 0.5).bfloat16()
+    idx = torch.full((T, k), -1, device=DEV, dtype=torch.int32)
+    lse = torch.zeros(T, 128, device=DEV)
+    want = torch.zeros(batch, ctx, device=DEV, dtype=torch.float64)
+    tol, count = torch.zeros_like(want), torch.zeros_like(want)
+    for b in range(batch):
+        c = kv[b].double()
+        for t in range(start[b], start[b + 1]):
+            pos = lens[b] - rows[b] + t - int(start[b])
+            n = min(k, pos + 1)
+            s = torch.randperm(pos + 1, device=DEV, generator=g)[:n].sort().values
+            idx[t, :n] = s.int()
+            z = q[t].double() @ c[s].T * scale
+            lse[t] = torch.logsumexp(z, 1)
+            w = torch.exp(z - lse[t].double()[:, None])
+            dz = 2 * 576 * 2.0 ** -24 * scale * (q[t].double().abs() @ c[s].abs().T) + \
+                (z.abs() + lse[t].double().abs()[:, None]) * 2.0 ** -22 + 2.0 ** -21
+            want[b, s] += w.mean(0)
+            tol[b, s] += (w * torch.expm1(dz)).mean(0) + w.mean(0) * 130 * 2.0 ** -24 + 2.0 ** -41
+    mass = torch.zeros(batch, ctx, device=DEV)
+    lay = dsa.KvLayout(batch, ctx, torch.tensor(lens, device=DEV, dtype=torch.int32))
+    starts = torch.tensor(start.tolist(), device=DEV, dtype=torch.int32)
+    dsa.dsa_attn_mass(q, kv, lay, per, idx, scale, lse, mass, q_start=starts)
+    assert dsa.dsa_get_device_error() == 0
+    assert batch * per >= 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    assert torch.all((mass.double() - want).abs() <= tol + 2.0 ** -23 * want)
+    assert float((mass.double().sum() - T).abs()) <= T * 1e-5

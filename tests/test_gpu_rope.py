@@ -186,3 +186,37 @@ def test_no_rows_special_values_streams_and_graphs():
     graph.replay()
     assert torch.equal(out, dsa.dsa_rope(x, pos, f))
     assert torch.equal(dx, dsa.dsa_rope_bwd(out, pos, f))
+
+
+@pytest.mark.parametrize("dtype,interleaved,rows,heads,dim,rot_begin,rot,offset", [
+    # on 148 SMs, calls that give a thread eight heads: 2.4 million units and more, in place too
+    (torch.bfloat16, False, 9600, 64, 128, 0, 64, 0),
+    (torch.float32, True, 1201, 128, 192, 128, 64, 0),
+    (torch.bfloat16, True, 8192, 61, 64, 0, 64, 0),    # heads past the last eight of a thread
+    (torch.float16, True, 3001, 131, 128, 16, 96, 0),
+    (torch.float16, False, 2200, 37, 67, 3, 64, 3),    # no 16-byte alignment
+    (torch.float32, True, 721, 107, 65, 1, 64, 1),
+    (torch.float32, False, 40, 250, 520, 1, 512, 0),   # a row's units over several blocks
+])
+def test_large_calls_equal_small_ones(dtype, interleaved, rows, heads, dim, rot_begin, rot, offset):
+    """Forward, backward and in place, bit for bit what calls of few rows give (a thread then takes
+    one head), and a sample of rows against the oracle."""
+    g = torch.Generator(device=DEV).manual_seed(rows + heads)
+    x = torch.empty(rows, heads, offset + dim, device=DEV, dtype=dtype)
+    x = x.normal_(generator=g)[..., offset:]
+    pos = torch.randint(-5, 1 << 20, (rows,), device=DEV, generator=g, dtype=torch.int32)
+    f, m = dsa.rope_freqs(rot, scaling="yarn", factor=32.0, device=DEV)
+    kw = dict(rot_begin=rot_begin, interleaved=interleaved, magnitude=m)
+    y, dx = dsa.dsa_rope(x, pos, f, **kw), dsa.dsa_rope_bwd(x, pos, f, **kw)
+    few = max(1, 100000 // (heads * dim))
+    for r in range(0, rows, few):
+        part = slice(r, r + few)
+        assert torch.equal(y[part], dsa.dsa_rope(x[part], pos[part], f, **kw))
+        assert torch.equal(dx[part], dsa.dsa_rope_bwd(x[part], pos[part], f, **kw))
+    at = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1], device=DEV)
+    kw.pop("magnitude")
+    _check(x[at], pos[at], f, m, y[at], **kw)
+    _check(x[at], pos[at], f, m, dx[at], backward=True, **kw)
+    dsa.dsa_rope(x, pos, f, x, magnitude=m, **kw)
+    assert torch.equal(x, y)
+    assert dsa.dsa_get_device_error() == 0
