@@ -645,8 +645,12 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
 def _rope(where, x, positions, freqs, out, rot_begin, interleaved, magnitude, stream):
     if x.dtype not in _DTYPES:
         raise ValueError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    if (x.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled():
+        raise ValueError(f"{where} records no gradient: pass detached tensors, and take the "
+                         "gradient from dsa_rope_bwd")
     dev = _device(x)
-    if out is None:
+    given = out is not None
+    if not given:
         out = _new(x.shape, x.dtype, x, stream)
     elif out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != dev:
         raise ValueError("out must have x's shape, type and device")
@@ -669,6 +673,8 @@ def _rope(where, x, positions, freqs, out, rot_begin, interleaved, magnitude, st
         _call(where, dev, stream, x.data_ptr(),
               _need("positions", positions, torch.int32, (rows,), dev),
               _need("freqs", freqs, torch.float64, None, dev), ctypes.byref(d), out.data_ptr())
+        if given and not out.is_inference():  # autograd may have saved what it held
+            torch.autograd.graph.increment_version(out)
     return out
 
 
@@ -676,8 +682,9 @@ def dsa_rope(x, positions, freqs, out=None, rot_begin: int = 0, interleaved: boo
              magnitude: float = 1.0, stream=None) -> torch.Tensor:
     """Rotary positions on dims [rot_begin, rot_begin + 2 len(freqs)) of every head of x
     [rows, dim] or [rows, heads, dim] (strided views allowed); ``out=x`` works in place.
-    positions int32 [rows]; freqs, magnitude a factor on those dims (include/dsa.h,
-    ``rope_freqs``)."""
+    positions int32 [rows]; magnitude a factor on those dims (include/dsa.h, ``rope_freqs``).
+    No gradient is recorded (a tensor that requires one is refused outside no_grad):
+    ``dsa_rope_bwd`` is its backward pass."""
     return _rope("dsa_rope", x, positions, freqs, out, rot_begin, interleaved, magnitude, stream)
 
 

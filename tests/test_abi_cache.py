@@ -317,3 +317,15 @@ def test_binding_refuses_wrong_tensors():
         dsa.dsa_evict_select(torch.zeros(2, 63), kv, 8)
     with pytest.raises(ValueError):
         dsa.dsa_evict_select(torch.zeros(2, 64), kv, 8)  # not on a GPU
+
+
+def test_rope_refuses_to_drop_a_gradient():
+    x = torch.zeros(2, 4, 64, requires_grad=True)
+    args = (torch.zeros(2, dtype=torch.int32), torch.zeros(32, dtype=torch.float64))
+    for call in (dsa.dsa_rope, dsa.dsa_rope_bwd):
+        with pytest.raises(ValueError, match="gradient"):
+            call(x, *args)
+        with pytest.raises(ValueError, match="gradient"):
+            call(x.detach(), *args, x)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call(x, *args)

@@ -220,3 +220,31 @@ def test_large_calls_equal_small_ones(dtype, interleaved, rows, heads, dim, rot_
     dsa.dsa_rope(x, pos, f, x, magnitude=m, **kw)
     assert torch.equal(x, y)
     assert dsa.dsa_get_device_error() == 0
+
+
+def test_written_tensors_are_known_to_autograd():
+    """A tensor that autograd saved and rope then wrote: its backward pass says so instead of
+    using the new values. dsa_rope_bwd inside a torch.autograd.Function, as a training program
+    would have it, gives the transposed turn."""
+    f, m = dsa.rope_freqs(64, device=DEV)
+    pos = torch.arange(6, device=DEV, dtype=torch.int32)
+    x = torch.randn(6, 2, 64, device=DEV)
+    w = torch.randn(6, 2, 64, device=DEV, requires_grad=True)
+    y = (w * x).sum()
+    dsa.dsa_rope(x, pos, f, x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        z = torch.randn(6, 2, 64, device=DEV)
+        dsa.dsa_rope(z, pos, f, z)
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return dsa.dsa_rope(x, pos, f)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return dsa.dsa_rope_bwd(dy, pos, f)
+    (Rope.apply(w) * x).sum().backward()
+    assert torch.equal(w.grad, dsa.dsa_rope_bwd(x, pos, f))
