@@ -39,12 +39,20 @@ KERNEL_HEADER = {"indexer": "indexer.cuh", "topk": "topk.cuh", "sparse_mla": "sp
                  "attn_mass": "attn_mass.cuh", "evict_select": "evict.cuh"}
 
 
+# what such a header includes beside the shared PTX and row helpers
+INCLUDED = {"cache.cuh": ["rope.cuh"]}
+
+
 def source_digest(kernel=None) -> str:
     """Digest of the CUDA sources and the ABI header (identifies a library build);
-    with ``kernel``, of that kernel's header and the shared PTX and row helpers only."""
+    with ``kernel``, of that kernel's header, what it includes, and the shared PTX and row
+    helpers only."""
     import hashlib
     h = hashlib.sha256()
-    files = (["ptx.cuh", "rows.cuh", KERNEL_HEADER[kernel]] if kernel else SOURCES + HEADERS)
+    files = SOURCES + HEADERS
+    if kernel:
+        header = KERNEL_HEADER[kernel]
+        files = ["ptx.cuh", "rows.cuh", *INCLUDED.get(header, []), header]
     for f in files:
         h.update(open(os.path.join(CSRC, f), "rb").read())
     if not kernel:

@@ -52,3 +52,26 @@ def test_no_kernel_spills(ptxas_report):
         m = re.search(r"(\d+) bytes spill stores, (\d+) bytes spill loads", text)
         assert m, f"no spill report for {name}"
         assert m.group(1) == "0" and m.group(2) == "0", f"{name} spills: {m.group(0)}"
+
+
+def test_a_kernels_digest_covers_what_its_header_includes(monkeypatch):
+    import builtins
+    from sparse_attention_05_b200 import build
+    read = []
+    real = builtins.open
+
+    def opened(path, *a, **kw):
+        read.append(os.path.basename(path))
+        return real(path, *a, **kw)
+    for kernel, header in build.KERNEL_HEADER.items():
+        read.clear()
+        monkeypatch.setattr(builtins, "open", opened)
+        build.source_digest(kernel)
+        monkeypatch.setattr(builtins, "open", real)
+        todo, seen = [header], set()
+        while todo:
+            name = todo.pop()
+            seen.add(name)
+            text = real(os.path.join(build.CSRC, name)).read()
+            todo += [n for n in re.findall(r'#include "([^"/]+)"', text) if n not in seen]
+        assert seen <= set(read), kernel
