@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
 // Moving in place: kept is ascending, so kept[i] >= i, and a chunk's destinations lie
 // below every later chunk's sources. A cluster of CTAs takes a column slice of a sequence
 // through its chunks in order: it loads a chunk into shared memory, waits at the cluster's
-// barrier until all its CTAs have theirs, and stores it; the next chunk's loads are issued
-// before that wait. The slices are independent of each other: nine of 128 B of the latent
+// barrier until all its CTAs have theirs, and stores it, while the next chunk's loads are under
+// way or done. The slices are independent of each other: nine of 128 B of the latent
 // row, one of the key row, one of scale and mass.
 // Into other pages the rows need no order: a warp takes up to 16 of them whole, four at a time
 // (1280 B of latent and key in 16-byte pieces, ten of a lane in flight): 48 sequences of 8192
@@ -218,20 +218,24 @@ __global__ void __launch_bounds__(kCompactThreads, 3) cache_move_kernel(const Co
       p.to_mass[(int64_t)b * p.to_mass_ld + z] = 0.f;
 }
 
-// All CTAs of the cluster have their chunk: this thread's copies have arrived. What has to be
-// ordered is one CTA's loads before another's stores to the same slots, which takes a release
-// and an acquire. The release waits for the releasing threads' own stores, so the last warp,
-// which moves nothing, gives it for its CTA, whose other warps have met it at the block's
-// barrier (8 sequences of 16384 kept tokens 68 us, and 80 with a release by every warp). A
-// cluster of one CTA needs the block's barrier alone.
-__device__ __forceinline__ void cluster_loaded(bool mover, int splits) {
+// What has to be ordered is one CTA's loads of a chunk before another's stores to the same
+// slots, which takes a release and an acquire. A release also waits for the stores before it, so
+// it is given for chunk c + 1 before chunk c is stored: then the stores before it are chunk
+// c - 1's, long done (8 paged sequences of 16384 kept tokens 79 us; 84 where a CTA arrives for
+// a chunk right before it stores it). The last warp, which moves nothing, gives it for its CTA,
+// whose other warps have met it at the block's barrier (contiguous, 74 us, 80 with a release by
+// every warp, and 68 with none: what the order costs). A cluster of one CTA needs the block's
+// barrier alone.
+__device__ __forceinline__ void chunk_loaded(bool mover, int splits) {
   __syncthreads();
   if (splits == 1) return;
   if (mover)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   else
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void chunk_loaded_by_all(int splits) {
+  if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int kEntries>
@@ -293,12 +297,15 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
     };
     int row[kEntries], next[kEntries], dst[kEntries];
     load(0, row);
+    load(1, next);
+    cp_async_wait_group<1>();
+    if (chunks > 0) chunk_loaded(mover, p.splits);
     for (int c = 0; c < chunks; ++c) {
-      load(c + 1, next);
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
-      cp_async_wait_group<1>();
-      cluster_loaded(mover, p.splits);  // all have loaded chunk c
+      cp_async_wait_group<0>();  // this thread's part of chunk c + 1
+      chunk_loaded_by_all(p.splits);
+      if (c + 1 < chunks) chunk_loaded(mover, p.splits);
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) {
 #pragma unroll
@@ -309,6 +316,7 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
         }
         row[e] = next[e];
       }
+      load(c + 2, next);
     }
     return;
   }
@@ -330,13 +338,16 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
   };
   int row[kEntries], next[kEntries];
   load(0, row);
+  load(1, next);
+  cp_async_wait_group<1>();
+  if (chunks > 0) chunk_loaded(mover, p.splits);
   for (int c = 0; c < chunks; ++c) {
-    load(c + 1, next);
     int dst[kEntries];
 #pragma unroll
     for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
-    cp_async_wait_group<1>();
-    cluster_loaded(mover, p.splits);
+    cp_async_wait_group<0>();
+    chunk_loaded_by_all(p.splits);
+    if (c + 1 < chunks) chunk_loaded(mover, p.splits);
 #pragma unroll
     for (int e = 0; e < kEntries; ++e) {
       if (dst[e] >= 0) {
@@ -346,6 +357,7 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
       }
       row[e] = next[e];
     }
+    load(c + 2, next);
   }
   if (p.mass && mover)
     for (int i = n + rank * kCompactThreads + tid; i < min(len, p.to_max_ctx);

@@ -1001,11 +1001,11 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
 
 // ---- compact -----------------------------------------------------------------------
 // In place: CTAs per slice, which form a cluster (of at most eight, the portable size) and move
-// its chunks in order; four for every SM (8 sequences of 16384 kept tokens: clusters of four 68
-// us, of eight 74; 20 of 8192: of two 82, of four 96). Two slices an SM and more go without
-// clusters, whose barrier costs more than it gives then (32 sequences of 8192 kept tokens: one
-// CTA a slice 113 us, two 125; 48: 146 and 166). Where the clusters leave SMs idle they take
-// chunks of twice the rows, half as many steps.
+// its chunks in order; six for every SM, of which three are resident: fewer serve equal lengths
+// better, more uneven ones (14 sequences of 8192 kept tokens, all of 16384 and of 4096 to 16384:
+// clusters of two 69 and 57 us, of four 73 and 47, of eight 72 and 49; 25: of one 123 and 105,
+// of four 118 and 83). Where the clusters leave SMs idle they take chunks of twice the rows,
+// half as many steps.
 template <int kEntries>
 dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream_t stream) {
   static DeviceOnce once;
@@ -1043,8 +1043,7 @@ dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStre
   }
   const int64_t chunks = (p.keep + kCompactRows - 1ll) / kCompactRows;
   const int64_t slices = (int64_t)batch * kCompactSlices;
-  const int64_t fill = slices >= 2 * num_sms() ? 1 : (4 * num_sms() + slices - 1) / slices;
-  p.splits = (int)std::min(chunks, fill);
+  p.splits = (int)std::min(chunks, (6 * num_sms() + slices - 1) / slices);
   p.splits = p.splits >= 8 ? 8 : p.splits >= 4 ? 4 : p.splits >= 2 ? 2 : 1;
   return slices * p.splits <= num_sms()
              ? launch_compact_kernel<2>(p, batch, stream)
