@@ -118,9 +118,12 @@ __global__ void __launch_bounds__(kAppendWarps * 32) cache_append_kernel(const A
 constexpr int kCompactThreads = 256;
 constexpr int kCompactBlock = kCompactThreads + 32;  // in place: and a warp for the barriers
 constexpr int kCompactSlices = 11;
-// A CTA's chunk in place: 256 or 512 rows (one or two entries of a lane), two of them in shared memory.
+// A CTA's chunk in place: 256 or 512 rows (one or two entries of a lane), two or three of them
+// in shared memory.
 constexpr int kCompactRows = kCompactThreads;
-constexpr int compact_smem_bytes(int entries) { return 2 * entries * kCompactRows * 128; }
+constexpr int compact_smem_bytes(int entries, int buffers) {
+  return buffers * entries * kCompactRows * 128;
+}
 
 struct CompactParams {
   const uint8_t* kv;
@@ -238,7 +241,8 @@ __device__ __forceinline__ void chunk_loaded_by_all(int splits) {
   if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int kEntries>
+// kBuffers: with three the loads of chunk c + 2 are issued before chunk c is stored, else after.
+template <int kEntries, int kBuffers>
 __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const CompactParams p) {
   extern __shared__ uint4 compact_smem[];
   const int b = blockIdx.x / p.splits, rank = blockIdx.x % p.splits;
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
     uint8_t* to = (slice < 9 ? p.to_kv + slice * 128 : p.to_k_idx) + piece * 16;
     // a lane's pieces in shared memory: + 32 a group of four rows, + kCompactRows * 8 an entry
     uint4* mine = compact_smem + (warp * 32 + sub) * 8 + piece;
-    auto buffer = [&](int c) { return mine + (c & 1) * kEntries * kCompactRows * 8; };
+    auto buffer = [&](int c) { return mine + (c % kBuffers) * kEntries * kCompactRows * 8; };
     auto load = [&](int c, int (&row)[kEntries]) {
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) {
@@ -295,15 +299,16 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
       }
       cp_async_commit();
     };
-    int row[kEntries], next[kEntries], dst[kEntries];
+    int row[kEntries], next[kEntries], far[kEntries] = {}, dst[kEntries];
     load(0, row);
     load(1, next);
     cp_async_wait_group<1>();
     if (chunks > 0) chunk_loaded(mover, p.splits);
     for (int c = 0; c < chunks; ++c) {
+      if (kBuffers == 3) load(c + 2, far);
 #pragma unroll
       for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
-      cp_async_wait_group<0>();  // this thread's part of chunk c + 1
+      cp_async_wait_group<kBuffers - 2>();  // this thread's part of chunk c + 1
       chunk_loaded_by_all(p.splits);
       if (c + 1 < chunks) chunk_loaded(mover, p.splits);
 #pragma unroll
@@ -314,15 +319,15 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
           if (r >= 0)
             *reinterpret_cast<uint4*>(to + r * pitch) = buffer(c)[e * kCompactRows * 8 + j * 32];
         }
-        row[e] = next[e];
+        row[e] = next[e], next[e] = far[e];
       }
-      load(c + 2, next);
+      if (kBuffers == 2) load(c + 2, next);
     }
     return;
   }
   // scale and mass, 4 B each
   float* mine = reinterpret_cast<float*>(compact_smem) + tid;
-  auto buffer = [&](int c, int e) { return mine + ((c & 1) * kEntries + e) * 2 * kCompactThreads; };
+  auto buffer = [&](int c, int e) { return mine + ((c % kBuffers) * kEntries + e) * 2 * kCompactThreads; };
   auto load = [&](int c, int (&row)[kEntries]) {
 #pragma unroll
     for (int e = 0; e < kEntries; ++e) {
@@ -336,16 +341,17 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
     }
     cp_async_commit();
   };
-  int row[kEntries], next[kEntries];
+  int row[kEntries], next[kEntries], far[kEntries] = {};
   load(0, row);
   load(1, next);
   cp_async_wait_group<1>();
   if (chunks > 0) chunk_loaded(mover, p.splits);
   for (int c = 0; c < chunks; ++c) {
+    if (kBuffers == 3) load(c + 2, far);
     int dst[kEntries];
 #pragma unroll
     for (int e = 0; e < kEntries; ++e) dst[e] = row[e] >= 0 ? destination(entry(c, e)) : -1;
-    cp_async_wait_group<0>();
+    cp_async_wait_group<kBuffers - 2>();
     chunk_loaded_by_all(p.splits);
     if (c + 1 < chunks) chunk_loaded(mover, p.splits);
 #pragma unroll
@@ -355,9 +361,9 @@ __global__ void __launch_bounds__(kCompactBlock) cache_compact_kernel(const Comp
         if (p.mass)
           p.to_mass[(int64_t)b * p.to_mass_ld + entry(c, e)] = buffer(c, e)[kCompactThreads];
       }
-      row[e] = next[e];
+      row[e] = next[e], next[e] = far[e];
     }
-    load(c + 2, next);
+    if (kBuffers == 2) load(c + 2, next);
   }
   if (p.mass && mover)
     for (int i = n + rank * kCompactThreads + tid; i < min(len, p.to_max_ctx);

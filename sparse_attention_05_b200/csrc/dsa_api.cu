@@ -1005,20 +1005,21 @@ dsa_status_t launch_evict(EvictParams& p, int batch, cudaStream_t stream) {
 // better, more uneven ones (14 sequences of 8192 kept tokens, all of 16384 and of 4096 to 16384:
 // clusters of two 69 and 57 us, of four 73 and 47, of eight 72 and 49; 25: of one 123 and 105,
 // of four 118 and 83). Where the clusters leave SMs idle they take chunks of twice the rows,
-// half as many steps.
-template <int kEntries>
+// half as many steps, and while two CTAs an SM are enough a third chunk in shared memory (2
+// sequences of 65536 kept tokens 76 us, not 97; one of 16384 14.9, not 16.4).
+template <int kEntries, int kBuffers>
 dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t attr_err = once_per_device(once, [] {
-    return cudaFuncSetAttribute(cache_compact_kernel<kEntries>,
+    return cudaFuncSetAttribute(cache_compact_kernel<kEntries, kBuffers>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                compact_smem_bytes(kEntries));
+                                compact_smem_bytes(kEntries, kBuffers));
   });
   if (attr_err != cudaSuccess) return DSA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)batch * p.splits), kCompactSlices, 1);
   cfg.blockDim = dim3(kCompactBlock, 1, 1);
-  cfg.dynamicSmemBytes = compact_smem_bytes(kEntries);
+  cfg.dynamicSmemBytes = compact_smem_bytes(kEntries, kBuffers);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1027,7 +1028,7 @@ dsa_status_t launch_compact_kernel(const CompactParams& p, int batch, cudaStream
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, cache_compact_kernel<kEntries>, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, cache_compact_kernel<kEntries, kBuffers>, p));
 }
 
 dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStream_t stream) {
@@ -1045,9 +1046,10 @@ dsa_status_t launch_compact(CompactParams& p, int batch, bool in_place, cudaStre
   const int64_t slices = (int64_t)batch * kCompactSlices;
   p.splits = (int)std::min(chunks, (6 * num_sms() + slices - 1) / slices);
   p.splits = p.splits >= 8 ? 8 : p.splits >= 4 ? 4 : p.splits >= 2 ? 2 : 1;
-  return slices * p.splits <= num_sms()
-             ? launch_compact_kernel<2>(p, batch, stream)
-             : launch_compact_kernel<1>(p, batch, stream);
+  const int64_t ctas = slices * p.splits;
+  return ctas <= num_sms()        ? launch_compact_kernel<2, 3>(p, batch, stream)
+         : ctas <= 2ll * num_sms() ? launch_compact_kernel<1, 3>(p, batch, stream)
+                                   : launch_compact_kernel<1, 2>(p, batch, stream);
 }
 
 // ---- attention mass ----------------------------------------------------------------

@@ -390,7 +390,8 @@ def test_compact_moves_every_bit(paged, page, in_place, lens, keep):
     # in place, most tokens kept, so that what one chunk's rows are moved over is another's source;
     # on 148 SMs: one CTA a slice and 20 chunks; clusters of two, four and eight and several chunks
     (100, 5200, 5001, True, True), (100, 700, 513, False, True), (48, 6000, 5777, False, True),
-    (20, 9000, 8500, True, True), (4, 20000, 19500, False, True), (1, 40000, 39001, True, True),
+    (20, 9000, 8500, True, True), (4, 20000, 19500, False, True), (2, 30000, 29000, True, True),
+    (1, 40000, 39001, True, True),
     # into other pages, two to four steps of a warp
     (20, 1400, 1003, True, False), (20, 1300, 1150, False, False), (40, 1700, 1501, True, False),
 ])
