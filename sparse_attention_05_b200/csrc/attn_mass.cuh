@@ -255,7 +255,7 @@ struct MassBlock {
 };
 
 // kFull: every tile has 256 entries, so the copies need no test of how many there are (512 rows
-// of 2048 take 162 us with it, 174 without).
+// of 2048, calls in a graph: 174 us with it, 187 without).
 template <bool kFull>
 __global__ void __launch_bounds__(kMassThreads, 1)
     attn_mass_kernel(const __grid_constant__ MassParams p) {
